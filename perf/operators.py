@@ -152,7 +152,8 @@ def _plain_fp8(st):
     m, k = st["x"].shape
     kb = -(-k // BLOCK)
     p = _blocks(st["x"].float(), kb)
-    s = p.abs().amax(dim=2, keepdim=True).clamp_min(AMAX_MIN) / FP8_MAX
+    top = p.abs().amax(dim=2, keepdim=True).clamp_min(AMAX_MIN)
+    s = top / torch.full_like(top, FP8_MAX)  # the rounded quotient (a Python number would be multiplied as 1/448)
     codes = (p * (1.0 / s)).clamp(-FP8_MAX, FP8_MAX).to(torch.float8_e4m3fn)
     x = (codes.float() * s).view(m, kb * BLOCK)[:, :k]
     ws = st["ws"].repeat_interleave(BLOCK, 0)[:st["wq"].shape[0]].repeat_interleave(BLOCK, 1)[:, :k]
