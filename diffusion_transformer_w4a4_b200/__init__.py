@@ -6,13 +6,17 @@ Argument marshalling only: every step of the layer runs in the CUDA library
 CPU fallback: if libsvdq.so is missing or cannot be loaded, every call raises.
 
 Entry points keep the C names (svdq_prepare, svdq_pack, svdq_layer_create,
-svdq_forward, ..., and svdq_awq_* for the awq_w4a16 layer).  `SvdqLinear` and
-`AwqLinear` bundle them for nn.Linear-style use.
+svdq_forward, ..., svdq_awq_* for the awq_w4a16 layer, svdq_w8a8_* and svdq_fp8_*
+for the 8-bit layers).  `SvdqLinear`, `AwqLinear`, `W8A8Linear` and `Fp8Linear`
+bundle them for nn.Linear-style use.  svdq_qk_norm_rope and svdq_cross_attn, the
+steps between a block's projections, take torch tensors [batch, tokens, heads, dim].
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -129,6 +133,27 @@ _EXPORTS = {
                                       ctypes.c_size_t, ctypes.c_void_p]),
     "svdq_w8a8_forward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                                          ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "svdq_fp8_prepare": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                        ctypes.c_void_p]),
+    "svdq_fp8_packed_size": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]),
+    "svdq_fp8_pack": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t]),
+    "svdq_fp8_layer_create": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64, ctypes.c_int64,
+                                             ctypes.POINTER(ctypes.c_void_p)]),
+    "svdq_fp8_layer_destroy": (None, [ctypes.c_void_p]),
+    "svdq_fp8_workspace_size": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)]),
+    "svdq_fp8_quantize_act": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                             ctypes.c_size_t, ctypes.c_void_p]),
+    "svdq_fp8_gemm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_size_t, ctypes.c_void_p]),
+    "svdq_fp8_forward": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "svdq_fp8_read_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
+                                            ctypes.POINTER(ctypes.c_int)]),
+    # the argument structures are passed as packed bytes (see _ROPE_ARGS, _ATTN_ARGS)
+    "svdq_qk_norm_rope": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_char_p, ctypes.c_int64, ctypes.c_int64,
+                                         ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]),
+    "svdq_cross_attn": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_void_p]),
     "svdq_w8a8_read_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
                                              ctypes.POINTER(ctypes.c_int)]),
 }
@@ -655,3 +680,287 @@ class W8A8Linear:
         if h is not None and _lib is not None:
             _lib.svdq_w8a8_layer_destroy(h)
             self.handle = None
+
+
+# ----------------------------------------------------------------------------- FP8, one scale for each block of 128
+def svdq_fp8_prepare(W):
+    """Host: W [N,K] bf16 bits -> (E4M3 codes u8 [N,K], scales f32 [ceil(N/128), ceil(K/128)])."""
+    W = np.ascontiguousarray(W, np.uint16)
+    N, K = W.shape
+    codes = np.empty((N, K), np.uint8)
+    scales = np.empty(((N + 127) // 128, (K + 127) // 128), np.float32)
+    _check(lib().svdq_fp8_prepare(W.ctypes.data, N, K, codes.ctypes.data, scales.ctypes.data), "svdq_fp8_prepare")
+    return codes, scales
+
+
+def svdq_fp8_packed_size(N: int, K: int) -> int:
+    v = ctypes.c_size_t()
+    _check(lib().svdq_fp8_packed_size(N, K, ctypes.byref(v)), "svdq_fp8_packed_size")
+    return v.value
+
+
+def svdq_fp8_pack(wcodes, wscales, bias=None) -> np.ndarray:
+    wcodes = np.ascontiguousarray(wcodes, np.uint8)
+    wscales = np.ascontiguousarray(wscales, np.float32)
+    N, K = wcodes.shape
+    if wscales.shape != ((N + 127) // 128, (K + 127) // 128):
+        raise ValueError(f"expected scales [{(N + 127) // 128}, {(K + 127) // 128}], got {wscales.shape}")
+    b = None if bias is None else np.ascontiguousarray(bias, np.uint16)
+    if b is not None and b.shape != (N,):
+        raise ValueError(f"expected a bias [{N}], got {b.shape}")
+    size = svdq_fp8_packed_size(N, K)
+    blob = np.zeros(size, np.uint8)
+    _check(lib().svdq_fp8_pack(N, K, wcodes.ctypes.data, wscales.ctypes.data, None if b is None else b.ctypes.data,
+                               blob.ctypes.data, size), "svdq_fp8_pack")
+    return blob
+
+
+def svdq_fp8_layer_create(dev_blob, blob_bytes: int, N: int, K: int):
+    h = ctypes.c_void_p()
+    _check(lib().svdq_fp8_layer_create(_ptr(dev_blob), blob_bytes, N, K, ctypes.byref(h)), "svdq_fp8_layer_create")
+    return h
+
+
+def svdq_fp8_layer_destroy(h) -> None:
+    lib().svdq_fp8_layer_destroy(h)
+
+
+def svdq_fp8_workspace_size(h, M: int) -> int:
+    v = ctypes.c_size_t()
+    _check(lib().svdq_fp8_workspace_size(h, M, ctypes.byref(v)), "svdq_fp8_workspace_size")
+    return v.value
+
+
+def svdq_fp8_quantize_act(h, X, M: int, ws, stream=None) -> None:
+    _check(lib().svdq_fp8_quantize_act(h, _ptr(X), M, _ptr(ws), ws.numel(), _stream(stream)), "svdq_fp8_quantize_act")
+
+
+def svdq_fp8_gemm(h, M: int, Y, ws, stream=None) -> None:
+    _check(lib().svdq_fp8_gemm(h, M, _ptr(Y), _ptr(ws), ws.numel(), _stream(stream)), "svdq_fp8_gemm")
+
+
+def svdq_fp8_forward(h, X, M: int, Y, ws, stream=None) -> None:
+    _check(lib().svdq_fp8_forward(h, _ptr(X), M, _ptr(Y), _ptr(ws), ws.numel(), _stream(stream)), "svdq_fp8_forward")
+
+
+def svdq_fp8_read_status(h, M: int, ws) -> int:
+    v = ctypes.c_int()
+    _check(lib().svdq_fp8_read_status(h, M, _ptr(ws), ws.numel(), ctypes.byref(v)), "svdq_fp8_read_status")
+    return v.value
+
+
+class Fp8Linear:
+    """One FP8 layer with a scale for each block of 128, on `device` (default: the
+    current CUDA device), from E4M3 weight codes u8 [N,K] (svdq_fp8_prepare, or a
+    checkpoint's own), their scales f32 [ceil(N/128), ceil(K/128)] and an optional
+    bf16 bias (bits); `forward(x)` maps bf16 [M, K] to bf16 [M, N], enqueued with the
+    layer's device current.  Workspaces are cached per token count and used by one
+    call at a time (calls on several streams take one layer object each)."""
+
+    def __init__(self, wcodes, wscales, bias=None, device=None):
+        import torch
+
+        self.N, self.K = int(wcodes.shape[0]), int(wcodes.shape[1])
+        self.device = _layer_device(device)
+        self.blob = torch.from_numpy(svdq_fp8_pack(wcodes, wscales, bias)).to(self.device)
+        with torch.cuda.device(self.device):
+            self.handle = svdq_fp8_layer_create(self.blob, self.blob.numel(), self.N, self.K)
+        self._ws = {}
+
+    def workspace_size(self, M: int) -> int:
+        return svdq_fp8_workspace_size(self.handle, M)
+
+    def workspace(self, M: int):
+        import torch
+
+        if M not in self._ws:
+            self._ws[M] = torch.empty(self.workspace_size(M), dtype=torch.uint8, device=self.device)
+        return self._ws[M]
+
+    def forward(self, x, out=None, stream=None):
+        import torch
+
+        _check_input(x, self.K, self.device)
+        M = x.numel() // self.K
+        if out is None:
+            out = x.new_empty(M, self.N)
+        elif not (out.dtype == torch.bfloat16 and out.device == self.device and out.is_contiguous()
+                  and out.numel() == M * self.N):
+            raise ValueError(f"expected a contiguous bf16 output [{M}, {self.N}] on {self.device}")
+        ws = self.workspace(M)
+        with _on(self.device):
+            svdq_fp8_forward(self.handle, x, M, out, ws, stream)
+        return out
+
+    __call__ = forward
+
+    def status(self, M: int) -> int:
+        return svdq_fp8_read_status(self.handle, M, self.workspace(M))
+
+    def read_act(self, M: int):
+        """Activation codes u8 [M, K] and scales f32 [M, ceil(K/128)] from the workspace (after quantize_act)."""
+        ws = self.workspace(M).cpu().numpy()
+        ld, kb = (M + 127) // 128 * 128, (self.K + 127) // 128
+        at = (M * self.K + 1023) // 1024 * 1024
+        scales = ws[at:at + 4 * kb * ld].view(np.float32).reshape(kb, ld)[:, :M]
+        return dict(codes=ws[:M * self.K].reshape(M, self.K).copy(), scales=np.ascontiguousarray(scales.T))
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and _lib is not None:
+            _lib.svdq_fp8_layer_destroy(h)
+            self.handle = None
+
+
+# ----------------------------------------------------------------------------- between the projections
+_ROPE_ARGS = struct.Struct("P3qP3q3qPPqP")  # svdq_norm_rope_args
+_ATTN_ARGS = struct.Struct("P3qP3qP3qP3q6qPPqf4x")  # svdq_attn_args
+PAIRS = {"interleaved": 0, "halves": 1}
+_attn_status = {}
+
+
+def _on(device):
+    """A context with `device` current (nothing to do, and nothing spent, where it is already)."""
+    import torch
+
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def attn_status(device=None):
+    """The status word (int32 tensor of one element) that svdq_cross_attn and svdq_qk_norm_rope report to on
+    `device`, unless they are given another: 0, or the code of the first device-side failure (sticky)."""
+    import torch
+
+    device = _layer_device(device)
+    t = _attn_status.get(device.index)
+    if t is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the first call on a device makes its status word: make it before any stream capture")
+        with torch.cuda.device(device):
+            t = torch.zeros(1, dtype=torch.int32, device=device)
+            torch.cuda.current_stream().synchronize()  # before any other stream uses it
+        _attn_status[device.index] = t
+    return t
+
+
+def _check_heads(name, t, device=None):
+    import torch
+
+    if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a bf16 CUDA tensor [batch, tokens, heads, dim], got {t.dtype} {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} on {t.device}, q on {device}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def _check_aux(name, t, dtype, shape, device):
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+
+
+def _rope_args(name, x, y, weight, rope, positions, device):
+    import torch
+
+    b, s, h, d = x.shape
+    if y.shape != x.shape:
+        raise ValueError(f"{name}: output shape {tuple(y.shape)} for input {tuple(x.shape)}")
+    if weight is not None:
+        _check_aux(f"{name}_weight", weight, torch.bfloat16, (d,), device)
+    if positions is not None:
+        _check_aux("positions", positions, torch.int32, (b, s), device)
+    return _ROPE_ARGS.pack(x.data_ptr(), *x.stride()[:3], y.data_ptr(), *y.stride()[:3], b, s, h,
+                           0 if weight is None else weight.data_ptr(), 0 if rope is None else rope.data_ptr(),
+                           0 if rope is None else rope.shape[0], 0 if positions is None else positions.data_ptr())
+
+
+def svdq_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, *, eps=1e-6, rope=None, positions=None,
+                      pairs="interleaved", out_q=None, out_k=None, status=None, stream=None):
+    """RMS norm of each head of q [B,S,H,D] (and k, in the same launch) with an optional weight bf16 [D], then the
+    rotation by `rope` f32 [rows, rot/2, 2] (cosine, sine; the first rot elements of a head, in `pairs`
+    "interleaved" or "halves"): row positions[b, s] (int32 [B,S]), or row s without positions.  Any strided view
+    with contiguous heads (a slice of a fused projection's output); out_q / out_k may be q / k themselves.  Returns
+    the rotated q, or (q, k)."""
+    import torch
+
+    _check_heads("q", q)
+    device = q.device
+    rot = 0
+    if rope is not None:
+        if rope.dim() != 3 or rope.shape[2] != 2:
+            raise ValueError(f"rope: expected [rows, rot/2, 2], got {tuple(rope.shape)}")
+        _check_aux("rope", rope, torch.float32, rope.shape, device)
+        rot = 2 * rope.shape[1]
+    elif positions is not None:
+        raise ValueError("positions need a rope table")
+    if out_q is None:
+        out_q = q.new_empty(q.shape)
+    else:
+        _check_heads("out_q", out_q, device)
+    qa = _rope_args("q", q, out_q, q_weight, rope, positions, device)
+    ka = None
+    if k is not None:
+        _check_heads("k", k, device)
+        if k.shape[3] != q.shape[3]:
+            raise ValueError(f"heads of {q.shape[3]} (q) and {k.shape[3]} (k)")
+        if out_k is None:
+            out_k = k.new_empty(k.shape)
+        else:
+            _check_heads("out_k", out_k, device)
+        ka = _rope_args("k", k, out_k, k_weight, rope, positions, device)
+    if status is None:
+        status = _attn_status.get(device.index)
+        if status is None:
+            status = attn_status(device)
+    else:
+        _check_aux("status", status, torch.int32, (1,), device)
+    with _on(device):
+        _check(lib().svdq_qk_norm_rope(qa, ka, q.shape[3], rot, PAIRS[pairs], eps, status.data_ptr(), _stream(stream)),
+               "svdq_qk_norm_rope")
+    return out_q if k is None else (out_q, out_k)
+
+
+def svdq_cross_attn(q, k, v, *, kv_len=None, kv_mask=None, scale=None, out=None, status=None, stream=None):
+    """Attention of q [B,Sq,H,D] over k, v [B,Sk,Hkv,D] (bf16 views, contiguous heads; H a multiple of Hkv; batch
+    and heads of k and v may be expanded): softmax(scale q k^T) v over the first kv_len[b] keys (int32 [B]) with
+    kv_mask[b, t] nonzero (uint8 or bool [B,Sk]).  Rows without a key give 0.  scale defaults to 1/sqrt(D).
+    Returns bf16 [B,Sq,H,D]."""
+    import torch
+
+    _check_heads("q", q)
+    device = q.device
+    _check_heads("k", k, device)
+    _check_heads("v", v, device)
+    b, sq, h, d = q.shape
+    _, sk, hk, _ = k.shape
+    if k.shape != v.shape or k.shape[0] != b or k.shape[3] != d:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not fit")
+    if out is None:
+        out = q.new_empty(q.shape)
+    else:
+        _check_heads("out", out, device)
+        if out.shape != q.shape:
+            raise ValueError(f"out {tuple(out.shape)} for q {tuple(q.shape)}")
+    if kv_len is not None:
+        _check_aux("kv_len", kv_len, torch.int32, (b,), device)
+    mask, mask_ld = 0, 0
+    if kv_mask is not None:
+        if kv_mask.dtype not in (torch.uint8, torch.bool) or kv_mask.device != device or \
+                tuple(kv_mask.shape) != (b, sk) or (sk > 1 and kv_mask.stride(1) != 1):
+            raise ValueError(f"kv_mask: expected uint8 or bool [{b}, {sk}] on {device}, rows contiguous, got "
+                             f"{kv_mask.dtype} {tuple(kv_mask.shape)} on {kv_mask.device}")
+        mask, mask_ld = kv_mask.data_ptr(), kv_mask.stride(0)
+    if status is None:
+        status = _attn_status.get(device.index)
+        if status is None:
+            status = attn_status(device)
+    else:
+        _check_aux("status", status, torch.int32, (1,), device)
+    args = _ATTN_ARGS.pack(q.data_ptr(), *q.stride()[:3], k.data_ptr(), *k.stride()[:3], v.data_ptr(),
+                           *v.stride()[:3], out.data_ptr(), *out.stride()[:3], b, sq, sk, h, hk, d,
+                           0 if kv_len is None else kv_len.data_ptr(), mask, mask_ld,
+                           d ** -0.5 if scale is None else scale)
+    with _on(device):
+        _check(lib().svdq_cross_attn(args, status.data_ptr(), _stream(stream)), "svdq_cross_attn")
+    return out

@@ -1,0 +1,789 @@
+// Attention of queries over another sequence's keys and values (cross attention),
+//
+//   O[b,s,h,:] = sum_t p_t V[b,t,g,:] / sum_t p_t,   p_t = exp(scale Q[b,s,h,:] . K[b,t,g,:]),
+//
+// t over the keys that sample b keeps (t < kv_len[b], kv_mask[b,t] != 0), g = h / (heads / kv_heads).
+//
+// One pass over the keys with a running maximum m and sum l per row:
+//   m' = max(m, max_t s_t),  l' = l 2^(c (m - m')) + sum_t 2^(c (s_t - m')),  O' = O 2^(c (m - m')) + P V,
+// with c = scale log2(e).  The rescaling of O is left out while m' exceeds the maximum in use by
+// less than 2^kLazy in p (sums and O are binary32, so p up to 2^8 costs no precision).
+//
+// Tiles: 128 rows x 128 keys.  S = Q K^T (tcgen05.mma kind::f16, binary32 in tensor memory); one thread
+// per row takes its S row, writes P as bf16 over it, and P V reads P from tensor memory.  P is rounded
+// to bf16 because the product takes 16-bit operands; its sum l uses the unrounded values.  Two streams
+// of 128 rows run in turn, so that one's products overlap the other's exponentials:
+//   PAIR     many rows: the streams are two query tiles that share the key tiles (each key tile is read
+//            once for 256 rows); persistent, one CTA per SM.
+//   !PAIR    few rows: the streams are the even and odd key tiles of one query tile, joined at the end;
+//            and a cluster of up to 8 CTAs splits the keys further and joins through distributed shared
+//            memory, in a fixed order (one launch, no workspace, no atomics).
+// Rows of a tile are (token, query head of the group) pairs, so heads that share keys share their tiles.
+//
+// Masked keys: scores become -inf by selection, and the masked rows of V are zeroed in shared memory
+// before the product (0 x NaN would poison it).  Rows without a key give 0.
+#include <cuda_bf16.h>
+
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "sm100.cuh"
+#include "svdq_internal.h"
+
+namespace svdq {
+namespace {
+
+constexpr int kRows = 128, kKeys = 128;
+constexpr int kChunkBytes = 128 * 128;  // 128 rows of 64 bf16
+constexpr int kThreads = 384;           // warps 0-3, 4-7 softmax; 8 loads; 9 products; 10 masked rows of V
+constexpr float kLazy = 8.f;
+constexpr int kMaxSplit = 8;
+
+template <int DC>
+struct Geo {  // DC: 64-wide chunks of the head dimension
+  static constexpr int kSlots = DC == 2 ? 4 : 8;
+  static constexpr int kTile = DC * kChunkBytes;
+  static constexpr int kPartLd = 64 * DC + 4;
+  static constexpr size_t kSmem = 1024 + (size_t)(2 + kSlots) * kTile + 4 * 128 * 4 + 512;
+  static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert(128 * kPartLd * 4 <= kSlots * kTile, "partial results fit the key/value ring");
+};
+
+struct AttnParams {
+  int sq, sk, hq, hk, d;
+  int group;       // query heads packed into the rows of a tile
+  int tok_tile;    // tokens per 128-row tile: 128 / group
+  int row_tiles;   // work items per (sample, item head): tiles (or pairs of tiles) of tokens
+  int heads_it;    // item heads: hq / group
+  int items;
+  int ksteps;      // ceil(d / 16)
+  int npv;         // d rounded up to 16
+  int splits;
+  int q_bm, q_hm, k_bm, k_hm, v_bm, v_hm;  // 0 where that dimension is broadcast (or of size one)
+  float c;                                 // scale * log2(e)
+  const int* kv_len;
+  const uint8_t* kv_mask;
+  long long mask_ld, mask_extent;
+  uint16_t* out;
+  long long o_sb, o_st, o_sh, out_extent;  // elements; extent in bytes
+  int batch;
+  int* status;
+  unsigned long long limit;
+};
+struct AttnMaps {
+  CUtensorMap q, k, v;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ int keys_of(const AttnParams& p, int b) {
+  if (!p.kv_len) return p.sk;
+  if (!SVDQ_INB(p.status, 4ll * b, 4, 4ll * p.batch)) return 0;
+  const int n = p.kv_len[b];
+  return n < 0 ? 0 : (n > p.sk ? p.sk : n);
+}
+
+// Bits of the 128 keys of tile t that count (the same in every lane).
+__device__ __forceinline__ void key_words(const AttnParams& p, int b, int t, int nkeys, int lane, uint32_t (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int key = t * kKeys + 32 * i + lane;
+    bool on = key < nkeys;
+    if (on && p.kv_mask) {
+      const long long at = (long long)b * p.mask_ld + key;
+      on = SVDQ_INB(p.status, at, 1, p.mask_extent) && p.kv_mask[at] != 0;
+    }
+    w[i] = __ballot_sync(0xffffffffu, on);
+  }
+}
+
+// One work item: sample, item head, first token of stream 0, key tiles.
+struct Item {
+  int b, h, tok0, nkeys, t0, t1;
+  bool second;  // PAIR: the second query tile has rows
+};
+template <bool PAIR>
+__device__ __forceinline__ Item item_of(const AttnParams& p, int item, int split) {
+  Item it;
+  const int rt = item % p.row_tiles;
+  const int bh = item / p.row_tiles;
+  it.h = bh % p.heads_it;
+  it.b = bh / p.heads_it;
+  it.tok0 = rt * p.tok_tile * (PAIR ? 2 : 1);
+  it.nkeys = keys_of(p, it.b);
+  const int n = (it.nkeys + kKeys - 1) / kKeys;
+  const int per = (n + p.splits - 1) / p.splits;
+  it.t0 = min(split * per, n);
+  it.t1 = min(it.t0 + per, n);
+  it.second = PAIR && it.tok0 + p.tok_tile < p.sq;
+  return it;
+}
+
+// Ring position (relative to the item's first) of stream s's tile in iteration i.
+template <bool PAIR>
+__device__ __forceinline__ int ring_pos(int i, int s, bool is_v, int n) {
+  if (PAIR) return 2 * i + (is_v ? 1 : 0);
+  const bool both = 2 * i + 1 < n;  // this iteration has a tile for each stream
+  return 4 * i + (is_v ? (both ? 2 : 1) : 0) + s;
+}
+
+template <bool PAIR, int DC>
+__global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ AttnMaps maps,
+                                                      const __grid_constant__ AttnParams p) {
+  using G = Geo<DC>;
+  constexpr int SLOTS = G::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sm_q = smem;                   // [2][tile]
+  uint8_t* sm_kv = smem + 2 * G::kTile;   // [SLOTS][tile]
+  float* sm_m = (float*)(sm_kv + SLOTS * G::kTile);  // [2][128]
+  float* sm_l = sm_m + 256;                          // [2][128]
+  uint64_t* q_full = (uint64_t*)(sm_l + 256);        // [2]
+  uint64_t* q_empty = q_full + 2;                    // [2]
+  uint64_t* kv_full = q_empty + 2;                   // [SLOTS]
+  uint64_t* kv_empty = kv_full + SLOTS;              // [SLOTS]
+  uint64_t* v_fixed = kv_empty + SLOTS;              // [SLOTS]
+  uint64_t* s_full = v_fixed + SLOTS;                // [2]
+  uint64_t* p_full = s_full + 2;                     // [2]
+  uint64_t* o_full = p_full + 2;                     // [2]
+  uint64_t* mma_done = o_full + 2;
+  uint32_t* tmem_slot = (uint32_t*)(mma_done + 1);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  WaitCtl wc{abort_flag, p.status, p.limit};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 4);  // one arrival per softmax warp of the stream
+      mbar_init(&o_full[s], 1);
+    }
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+      mbar_init(&v_fixed[s], 1);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  // An earlier kernel that let this one start may still need tensor memory on this SM: allocate behind it.
+  pdl_wait();
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;  // S0/P0 | S1/P1 | O0 | O1, 128 columns each
+
+  const bool fixing = p.kv_len != nullptr || p.kv_mask != nullptr;
+  const int split = PAIR ? 0 : (p.splits > 1 ? (int)cluster_ctarank() : 0);
+  const int item0 = PAIR ? (int)blockIdx.x : (int)blockIdx.x / p.splits;
+  const int item_step = PAIR ? (int)gridDim.x : p.items;  // !PAIR: one item per cluster
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ loads
+    if (lane == 0) {
+      prefetch_tmap(&maps.q);
+      prefetch_tmap(&maps.k);
+      prefetch_tmap(&maps.v);
+      int pos = 0;       // ring position of the next tile
+      int nq[2] = {0, 0};  // query tiles loaded per stream
+      bool ok = true;
+      auto load_kv = [&](const CUtensorMap* map, int head, int bat, int t) {
+        const int s = pos % SLOTS;
+        if (!mbar_wait(&kv_empty[s], ((pos / SLOTS) & 1) ^ 1, wc)) return false;
+        mbar_arrive_expect_tx(&kv_full[s], G::kTile);
+#pragma unroll
+        for (int ch = 0; ch < DC; ++ch)
+          tma_load_4d(map, &kv_full[s], sm_kv + s * G::kTile + ch * kChunkBytes, 64 * ch, head, t * kKeys, bat);
+        ++pos;
+        return true;
+      };
+      const uint32_t q_bytes = (uint32_t)(DC * 128 * p.group * p.tok_tile);
+      for (int item = item0; item < p.items && ok; item += item_step) {
+        const Item it = item_of<PAIR>(p, item, split);
+        const int n = it.t1 - it.t0;
+        if (n == 0) continue;
+        const int kvh = (int)((long long)it.h * p.group * p.hk / p.hq);
+        for (int s = 0; s < (it.second ? 2 : 1) && ok; ++s) {
+          if (!mbar_wait(&q_empty[s], (nq[s] & 1) ^ 1, wc)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&q_full[s], q_bytes);
+#pragma unroll
+          for (int ch = 0; ch < DC; ++ch)
+            tma_load_4d(&maps.q, &q_full[s], sm_q + s * G::kTile + ch * kChunkBytes, 64 * ch,
+                        it.h * p.group * p.q_hm, it.tok0 + s * p.tok_tile, it.b * p.q_bm);
+          ++nq[s];
+        }
+        if (PAIR) {
+          for (int t = it.t0; t < it.t1 && ok; ++t)
+            ok = load_kv(&maps.k, kvh * p.k_hm, it.b * p.k_bm, t) && load_kv(&maps.v, kvh * p.v_hm, it.b * p.v_bm, t);
+        } else {
+          for (int t = it.t0; t < it.t1 && ok; t += 2) {
+            const int two = t + 1 < it.t1 ? 2 : 1;
+            for (int s = 0; s < two && ok; ++s) ok = load_kv(&maps.k, kvh * p.k_hm, it.b * p.k_bm, t + s);
+            for (int s = 0; s < two && ok; ++s) ok = load_kv(&maps.v, kvh * p.v_hm, it.b * p.v_bm, t + s);
+          }
+        }
+      }
+      if (!ok) {  // drain copies still in flight
+        for (int j = (pos > SLOTS ? pos - SLOTS : 0); j < pos; ++j)
+          mbar_wait_drain(&kv_full[j % SLOTS], (j / SLOTS) & 1, p.limit);
+        for (int s = 0; s < 2; ++s)
+          if (nq[s]) mbar_wait_drain(&q_full[s], (nq[s] - 1) & 1, p.limit);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+      const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
+      const uint32_t idesc_o = idesc_bf16_f32(kRows, p.npv) | (1u << 16);  // B (= V) has the head dimension contiguous
+      int base = 0, fixes = 0;
+      int nq[2] = {0, 0}, np[2] = {0, 0};
+      bool ok = true;
+      auto slot_wait = [&](int pos) {
+        if (!mbar_wait(&kv_full[pos % SLOTS], (pos / SLOTS) & 1, wc)) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto issue_s = [&](int s, int pos) {
+        const uint32_t qa = smem_u32(sm_q + (PAIR ? s : 0) * G::kTile);
+        const uint32_t ka = smem_u32(sm_kv + (pos % SLOTS) * G::kTile);
+        for (int kk = 0; kk < p.ksteps; ++kk) {
+          const uint32_t off = (uint32_t)((kk >> 2) * kChunkBytes + (kk & 3) * 32);
+          mma_bf16(tmem + s * 128, make_sdesc(qa + off, 16, 1024, LAYOUT_SW128),
+                   make_sdesc(ka + off, 16, 1024, LAYOUT_SW128), idesc_s, kk != 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[s]);
+      };
+      auto issue_o = [&](int s, int pos, bool first) {
+        const uint32_t va = smem_u32(sm_kv + (pos % SLOTS) * G::kTile);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_bf16_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * kk,
+                      make_sdesc(va + 2048 * kk, kChunkBytes, 1024, LAYOUT_SW128), idesc_o,
+                      (first && kk == 0) ? 0u : 1u);
+      };
+      for (int item = item0; item < p.items && ok; item += item_step) {
+        const Item it = item_of<PAIR>(p, item, split);
+        const int n = it.t1 - it.t0;
+        if (n == 0) continue;
+        const int iters = PAIR ? n : (n + 1) / 2;
+        auto has = [&](int i, int s) { return PAIR ? (s == 0 || it.second) && i < n : 2 * i + s < n; };
+        for (int s = 0; s < 2 && ok; ++s) {
+          if (!has(0, s)) continue;
+          if (PAIR || s == 0) {
+            ok = mbar_wait(&q_full[s], nq[s] & 1, wc);
+            ++nq[s];
+          }
+          const int kp = base + ring_pos<PAIR>(0, s, false, n);
+          ok = ok && slot_wait(kp);
+          if (!ok) break;
+          issue_s(s, kp);
+          if (!PAIR || s == 1 || !it.second) umma_commit(&kv_empty[kp % SLOTS]);
+          if (PAIR && n == 1) umma_commit(&q_empty[s]);
+        }
+        for (int i = 0; i < iters && ok; ++i) {
+          for (int s = 0; s < 2 && ok; ++s) {
+            if (!has(i, s)) continue;
+            const int vp = base + ring_pos<PAIR>(i, s, true, n);
+            const bool last_user = !PAIR || s == 1 || !it.second;
+            if (!PAIR || s == 0) {
+              ok = slot_wait(vp);
+              if (ok && fixing) {
+                ok = mbar_wait(&v_fixed[fixes % SLOTS], (fixes / SLOTS) & 1, wc);
+                ++fixes;
+              }
+            }
+            ok = ok && mbar_wait(&p_full[s], np[s] & 1, wc);
+            if (!ok) break;
+            ++np[s];
+            tc_fence_after();
+            issue_o(s, vp, i == 0);
+            if (last_user) umma_commit(&kv_empty[vp % SLOTS]);
+            if (has(i + 1, s)) {
+              const int kp = base + ring_pos<PAIR>(i + 1, s, false, n);
+              if (!PAIR || s == 0) {
+                ok = slot_wait(kp);
+                if (!ok) break;
+              }
+              issue_s(s, kp);
+              if (last_user) umma_commit(&kv_empty[kp % SLOTS]);
+              if (PAIR && i + 2 == n) umma_commit(&q_empty[s]);
+            } else {
+              umma_commit(&o_full[s]);
+            }
+          }
+        }
+        base += 2 * n;
+      }
+      umma_commit(mma_done);
+      mbar_wait_drain(mma_done, 0, p.limit);
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ zero the masked rows of V
+    // Where keys can be masked, every V tile passes through here, so that this warp neither runs ahead
+    // of the ring nor falls behind it; rows past the last key of all are zeros already (the loads fill them).
+    int base = 0, fixes = 0;
+    bool ok = true;
+    for (int item = item0; item < p.items && ok && fixing; item += item_step) {
+      const Item it = item_of<PAIR>(p, item, split);
+      const int n = it.t1 - it.t0;
+      for (int j = 0; j < n && ok; ++j) {
+        const int t = it.t0 + j;
+        uint32_t w[4];
+        key_words(p, it.b, t, it.nkeys, lane, w);
+        const int pos = base + (PAIR ? ring_pos<PAIR>(j, 0, true, n) : ring_pos<PAIR>(j >> 1, j & 1, true, n));
+        ok = warp_wait(&kv_full[pos % SLOTS], (pos / SLOTS) & 1, wc);
+        if (!ok) break;
+        uint8_t* tile = sm_kv + (pos % SLOTS) * G::kTile;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t off = ~w[i];
+          while (off) {  // four rows at a time, eight lanes to a row's 128 bytes
+            uint32_t o2 = off;
+            for (int k = 0; k < (lane >> 3); ++k) o2 &= o2 - 1;
+            if (o2) {
+              const int row = 32 * i + __ffs(o2) - 1;
+#pragma unroll
+              for (int ch = 0; ch < DC; ++ch)
+                *(uint4*)(tile + ch * kChunkBytes + row * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) off &= off - 1;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_fixed[fixes % SLOTS]);
+        ++fixes;
+      }
+      base += 2 * n;
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax and output
+    const int st = warp >> 2, quarter = warp & 3;
+    const int row = 32 * quarter + lane;
+    const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
+    const uint32_t t_s = tmem + lanes + st * 128, t_o = tmem + lanes + 256 + st * 128;
+    const int r_tok = row / p.group, r_head = row - r_tok * p.group;
+    int ns = 0, no = 0;
+    bool ok = true;
+    for (int item = item0; item < p.items && ok; item += item_step) {
+      const Item it = item_of<PAIR>(p, item, split);
+      const int n = it.t1 - it.t0;
+      if (PAIR && st == 1 && !it.second) continue;
+      const int tok = it.tok0 + (PAIR ? st * p.tok_tile : 0) + r_tok;
+      const bool valid = r_tok < p.tok_tile && tok < p.sq;
+      const bool warp_valid = __any_sync(0xffffffffu, valid);
+      const int my = PAIR ? n : (n - st + 1) / 2;  // tiles of this stream
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; i < my && ok; ++i) {
+        const int t = it.t0 + (PAIR ? i : 2 * i + st);
+        const bool masked = p.kv_mask || it.nkeys < (t + 1) * kKeys;
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (masked) key_words(p, it.b, t, it.nkeys, lane, w);
+        ok = warp_wait(&s_full[st], ns & 1, wc);
+        if (!ok) break;
+        ++ns;
+        tc_fence_after();
+        if (warp_valid) {
+          uint32_t sr[4][32];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(t_s + 32 * k, sr[k]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld_wait_regs(sr[k]);
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                sr[k][j] = (w[k] >> j) & 1u ? sr[k][j] : 0xFF800000u;  // -inf
+          }
+          float mx = m;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(sr[k][j]));
+          if (i == 0) {
+            m = mx;
+          } else if (__any_sync(0xffffffffu, (mx - m) * p.c > kLazy)) {
+            const float f = mx == -INFINITY ? 1.f : ex2((m - mx) * p.c);
+            m = mx;
+            l *= f;
+            // every product of the previous tile is complete: S of this tile was issued after it
+            for (int cc = 0; cc < p.npv; cc += 16) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(t_o + cc, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st_32x32b_x16(t_o + cc, o);
+            }
+          }
+          const float mc = m == -INFINITY ? 0.f : m * p.c;
+          float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            uint32_t pr[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const uint32_t(&src)[32] = sr[k + (j >> 4)];
+              const float e0 = ex2(fmaf(__uint_as_float(src[2 * (j & 15)]), p.c, -mc));
+              const float e1 = ex2(fmaf(__uint_as_float(src[2 * (j & 15) + 1]), p.c, -mc));
+              l4[j & 3] += e0 + e1;
+              __nv_bfloat162 hv = __floats2bfloat162_rn(e0, e1);
+              pr[j] = *(uint32_t*)&hv;
+            }
+            tmem_st_32x32b_x32(t_s + 16 * k, pr);
+          }
+          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[st]);
+      }
+      if (PAIR) {
+        if (!ok) break;
+        if (n > 0) {
+          ok = warp_wait(&o_full[st], no & 1, wc);
+          if (!ok) break;
+          ++no;
+          tc_fence_after();
+        }
+        if (warp_valid) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;  // a row without a key: 0
+          const long long off = (long long)it.b * p.o_sb + (long long)tok * p.o_st +
+                                (long long)(it.h * p.group + r_head) * p.o_sh;
+          for (int cc = 0; cc < p.npv; cc += 16) {
+            uint32_t o[16];
+            if (n > 0) {
+              tmem_ld_32x32b_x16(t_o + cc, o);
+              tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = 0;
+            }
+            uint32_t y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              __nv_bfloat162 hv = l == 0.f ? __floats2bfloat162_rn(0.f, 0.f)
+                                           : __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv,
+                                                                   __uint_as_float(o[2 * j + 1]) * inv);
+              y[j] = *(uint32_t*)&hv;
+            }
+            if (valid) {
+#pragma unroll
+              for (int v = 0; v < 2; ++v)
+                if (cc + 8 * v < p.d && SVDQ_INB(p.status, 2 * (off + cc + 8 * v), 16, p.out_extent))
+                  *(uint4*)(p.out + off + cc + 8 * v) = make_uint4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
+            }
+          }
+          tc_fence_before();  // these loads come before the products that the next P lets start
+        }
+      } else {
+        // Join of the two streams: every thread of both arrives here once, also after an expired wait.
+        sm_m[st * 128 + row] = m;
+        sm_l[st * 128 + row] = l;
+        for (int s = 0; s < 2 && ok; ++s)
+          if (s < n) ok = warp_wait(&o_full[s], 0, wc);
+        ok = named_bar_and(1, 256, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const float m0 = sm_m[row], m1 = sm_m[128 + row];
+        const float mm = fmaxf(m0, m1);
+        const float f0 = m0 == -INFINITY ? 0.f : ex2((m0 - mm) * p.c);
+        const float f1 = m1 == -INFINITY ? 0.f : ex2((m1 - mm) * p.c);
+        const float ll = sm_l[row] * f0 + sm_l[128 + row] * f1;
+        const float inv = 1.f / ll;
+        float* part = (float*)sm_kv;
+        const long long off = (long long)it.b * p.o_sb + (long long)tok * p.o_st +
+                              (long long)(it.h * p.group + r_head) * p.o_sh;
+        if (warp_valid) {
+          for (int cc = 16 * st; cc < p.npv; cc += 32) {
+            uint32_t a[16], b[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) a[j] = b[j] = 0;
+            if (n > 0) tmem_ld_32x32b_x16(tmem + lanes + 256 + cc, a);
+            if (n > 1) tmem_ld_32x32b_x16(tmem + lanes + 384 + cc, b);
+            tmem_ld_wait();
+            float o[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = fmaf(__uint_as_float(a[j]), f0, __uint_as_float(b[j]) * f1);
+            if (p.splits > 1) {
+              if (valid) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+                  *(float4*)(part + row * G::kPartLd + cc + 4 * v) =
+                      make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+              }
+            } else if (valid) {
+#pragma unroll
+              for (int v = 0; v < 2; ++v) {
+                uint32_t y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  __nv_bfloat162 hv = ll == 0.f ? __floats2bfloat162_rn(0.f, 0.f)
+                                                : __floats2bfloat162_rn(o[8 * v + 2 * j] * inv, o[8 * v + 2 * j + 1] * inv);
+                  y[j] = *(uint32_t*)&hv;
+                }
+                if (cc + 8 * v < p.d && SVDQ_INB(p.status, 2 * (off + cc + 8 * v), 16, p.out_extent))
+                  *(uint4*)(p.out + off + cc + 8 * v) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+            }
+          }
+        }
+        named_bar_sync(1, 256);  // both streams have read m and l
+        if (st == 0) {
+          sm_m[row] = mm;
+          sm_l[row] = ll;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (!PAIR && p.splits > 1) {
+    // Join of the cluster's CTAs: each takes a share of the tile's outputs and reads every CTA's part.
+    const bool good = *abort_flag == 0;
+    cluster_sync();
+    if (good && item0 < p.items) {
+      const Item it = item_of<PAIR>(p, item0, split);
+      const int toks = min(p.tok_tile, p.sq - it.tok0);
+      const int per_row = p.d / 8;
+      const int total = toks * p.group * per_row;
+      const uint32_t part = smem_u32(sm_kv), pm = smem_u32(sm_m), pl = smem_u32(sm_l);
+      for (int idx = split * kThreads + threadIdx.x; idx < total; idx += p.splits * kThreads) {
+        const int row = idx / per_row, col = (idx - row * per_row) * 8;
+        float mr[kMaxSplit];
+        float mm = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r) {
+          mr[r] = r < p.splits ? dsmem_ld_f32(dsmem_addr(pm + 4 * row, r)) : -INFINITY;
+          mm = fmaxf(mm, mr[r]);
+        }
+        float ll = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r) {
+          if (r < p.splits) {
+            const float lr = dsmem_ld_f32(dsmem_addr(pl + 4 * row, r));
+            const uint32_t pa = dsmem_addr(part + (uint32_t)(row * G::kPartLd + col) * 4, r);
+            const float4 x = dsmem_ld_f32x4(pa), y = dsmem_ld_f32x4(pa + 16);
+            const float f = mr[r] == -INFINITY ? 0.f : ex2((mr[r] - mm) * p.c);
+            ll = fmaf(lr, f, ll);
+            o[0] = fmaf(x.x, f, o[0]);
+            o[1] = fmaf(x.y, f, o[1]);
+            o[2] = fmaf(x.z, f, o[2]);
+            o[3] = fmaf(x.w, f, o[3]);
+            o[4] = fmaf(y.x, f, o[4]);
+            o[5] = fmaf(y.y, f, o[5]);
+            o[6] = fmaf(y.z, f, o[6]);
+            o[7] = fmaf(y.w, f, o[7]);
+          }
+        }
+        const float inv = 1.f / ll;
+        uint32_t y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          __nv_bfloat162 hv = ll == 0.f ? __floats2bfloat162_rn(0.f, 0.f)
+                                        : __floats2bfloat162_rn(o[2 * j] * inv, o[2 * j + 1] * inv);
+          y[j] = *(uint32_t*)&hv;
+        }
+        const int tok = it.tok0 + row / p.group, head = it.h * p.group + row % p.group;
+        const long long off = (long long)it.b * p.o_sb + (long long)tok * p.o_st + (long long)head * p.o_sh + col;
+        if (SVDQ_INB(p.status, 2 * off, 16, p.out_extent)) *(uint4*)(p.out + off) = make_uint4(y[0], y[1], y[2], y[3]);
+      }
+    }
+    cluster_sync();  // a CTA's shared memory stays until every other has read it
+  }
+}
+
+template <bool PAIR, int DC>
+int launch(const AttnMaps& maps, const AttnParams& p, int dev, int grid, cudaStream_t stream) {
+  {  // the shared-memory attribute belongs to the kernel on each device: set it once per device
+    static std::mutex mu;
+    static bool attr_set[64] = {};
+    if (dev < 0 || dev >= 64) return SVDQ_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!attr_set[dev]) {
+      if (cudaFuncSetAttribute(k_attn<PAIR, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)Geo<DC>::kSmem) != cudaSuccess)
+        return SVDQ_ERR_CUDA;
+      attr_set[dev] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Geo<DC>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.splits > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_attn<PAIR, DC>, maps, p) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+}
+
+// Tensor map of a [batch, tokens, heads, dim] view.  A dimension of size one, or one with
+// stride 0 (broadcast), becomes a dimension of size one whose coordinate is always 0.
+int heads_map(CUtensorMap* map, const svdq_heads& h, int64_t batch, int64_t tokens, int64_t heads, int64_t dim,
+              uint32_t box_heads, uint32_t box_tokens, int* batch_mul, int* head_mul) {
+  *batch_mul = batch > 1 && h.stride_batch != 0;
+  *head_mul = heads > 1 && h.stride_head != 0;
+  const uint64_t any = (uint64_t)((dim * 2 + 15) / 16 * 16);
+  const uint64_t dims[4] = {(uint64_t)dim, *head_mul ? (uint64_t)heads : 1, (uint64_t)tokens,
+                            *batch_mul ? (uint64_t)batch : 1};
+  const uint64_t strides[3] = {*head_mul ? (uint64_t)h.stride_head * 2 : any,
+                               tokens > 1 ? (uint64_t)h.stride_token * 2 : any,
+                               *batch_mul ? (uint64_t)h.stride_batch * 2 : any};
+  const uint32_t box[4] = {64, box_heads, box_tokens, 1};
+  return encode_tmap_4d_bf16(map, h.data, dims, strides, box);
+}
+
+}  // namespace
+
+int check_heads(const svdq_heads& h, int64_t batch, int64_t tokens, int64_t heads, int64_t dim, bool out) {
+  if (!h.data || ((uintptr_t)h.data & 15)) return SVDQ_ERR_INVALID_ARG;
+  const int64_t size[3] = {batch, tokens, heads};
+  const int64_t stride[3] = {h.stride_batch, h.stride_token, h.stride_head};
+  int64_t span = dim;
+  for (int i = 0; i < 3; ++i) {
+    if (size[i] <= 1) continue;
+    if (stride[i] < 0 || stride[i] % 8 != 0 || stride[i] > ((int64_t)1 << 38)) return SVDQ_ERR_INVALID_ARG;
+    if (stride[i] == 0 && (out || i == 1)) return SVDQ_ERR_INVALID_ARG;
+    if (stride[i] != 0 && stride[i] < dim) return SVDQ_ERR_INVALID_ARG;  // elements of two places overlap
+    span += (size[i] - 1) * stride[i];
+    if (span > ((int64_t)1 << 40)) return SVDQ_ERR_INVALID_ARG;
+  }
+  return SVDQ_OK;
+}
+int64_t heads_extent(const svdq_heads& h, int64_t batch, int64_t tokens, int64_t heads, int64_t dim) {
+  int64_t span = dim;
+  if (batch > 1) span += (batch - 1) * h.stride_batch;
+  if (tokens > 1) span += (tokens - 1) * h.stride_token;
+  if (heads > 1) span += (heads - 1) * h.stride_head;
+  return 2 * span;
+}
+
+}  // namespace svdq
+
+using namespace svdq;
+
+extern "C" svdq_status svdq_cross_attn(const svdq_attn_args* a, int32_t* status, void* stream) {
+  if (!a || !status || ((uintptr_t)status & 3)) return SVDQ_ERR_INVALID_ARG;
+  const int64_t lim = (int64_t)1 << 30;
+  if (a->batch < 0 || a->q_tokens < 0 || a->kv_tokens < 0 || a->batch > lim || a->q_tokens > lim || a->kv_tokens > lim)
+    return SVDQ_ERR_INVALID_ARG;
+  if (a->heads < 1 || a->kv_heads < 1 || a->heads > 4096 || a->heads % a->kv_heads != 0) return SVDQ_ERR_INVALID_ARG;
+  if (a->dim < 8 || a->dim > 128 || a->dim % 8 != 0) return SVDQ_ERR_INVALID_ARG;
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return SVDQ_ERR_INVALID_ARG;
+  if (a->batch == 0 || a->q_tokens == 0) return SVDQ_OK;
+  int st = check_heads(a->o, a->batch, a->q_tokens, a->heads, a->dim, true);
+  if (st == SVDQ_OK) st = check_heads(a->q, a->batch, a->q_tokens, a->heads, a->dim, false);
+  if (st != SVDQ_OK) return (svdq_status)st;
+  // without a key there is nothing to read, and the maps below need a valid tensor: stand in the queries
+  const svdq_heads& kh = a->kv_tokens > 0 ? a->k : a->q;
+  const svdq_heads& vh = a->kv_tokens > 0 ? a->v : a->q;
+  if (a->kv_tokens > 0) {
+    st = check_heads(a->k, a->batch, a->kv_tokens, a->kv_heads, a->dim, false);
+    if (st == SVDQ_OK) st = check_heads(a->v, a->batch, a->kv_tokens, a->kv_heads, a->dim, false);
+    if (st != SVDQ_OK) return (svdq_status)st;
+  }
+  if (a->kv_mask && a->batch > 1 && a->mask_stride < 0) return SVDQ_ERR_INVALID_ARG;
+  if (((uintptr_t)a->kv_len & 3)) return SVDQ_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return SVDQ_ERR_UNSUPPORTED_DEVICE;
+  }
+  svdq_status sd = svdq_device_check(dev);
+  if (sd != SVDQ_OK) return sd;
+  const void* ptrs[7] = {a->q.data, kh.data, vh.data, a->o.data, a->kv_len, a->kv_mask, status};
+  for (const void* ptr : ptrs)
+    if (ptr && check_blob_pointer(ptr, dev) != SVDQ_OK) return SVDQ_ERR_INVALID_ARG;
+
+  AttnParams p{};
+  p.sq = (int)a->q_tokens;
+  p.sk = (int)a->kv_tokens;
+  p.hq = (int)a->heads;
+  p.hk = (int)a->kv_heads;
+  p.d = (int)a->dim;
+  p.batch = (int)a->batch;
+  const int share = p.hq / p.hk;
+  // Query heads of one key head go into the rows of one tile; a broadcast query head, or more
+  // of them than a tile has rows, is taken head by head.
+  p.group = share <= kRows && (share == 1 || a->q.stride_head != 0) ? share : 1;
+  p.tok_tile = kRows / p.group;
+  p.heads_it = p.hq / p.group;
+  p.ksteps = (p.d + 15) / 16;
+  p.npv = p.ksteps * 16;
+  p.c = a->scale * 1.4426950408889634f;
+  p.kv_len = a->kv_len;
+  p.kv_mask = a->kv_mask;
+  p.mask_ld = a->batch > 1 ? a->mask_stride : 0;
+  p.mask_extent = (a->batch - 1) * p.mask_ld + a->kv_tokens;
+  p.out = (uint16_t*)a->o.data;
+  p.o_sb = a->o.stride_batch;
+  p.o_st = a->o.stride_token;
+  p.o_sh = a->o.stride_head;
+  p.out_extent = heads_extent(a->o, a->batch, a->q_tokens, a->heads, a->dim);
+  p.status = status;
+  p.limit = wait_limit_cycles();
+
+  const int sms = device_sm_count(dev);
+  const int64_t bh = (int64_t)p.batch * p.heads_it;
+  const int64_t tiles = ((int64_t)p.sq + p.tok_tile - 1) / p.tok_tile;
+  const int64_t pairs = (tiles + 1) / 2;
+  const int ktiles = (p.sk + kKeys - 1) / kKeys;
+  // Pairs of tiles once they fill the SMs; below that single tiles, whose keys are split over the SMs
+  // that would stay idle, two key tiles to a CTA at least.
+  const bool pair = bh * pairs >= sms;
+  if (bh * tiles > ((int64_t)1 << 30)) return SVDQ_ERR_INVALID_ARG;
+  p.splits = 1;
+  if (!pair)
+    while (p.splits < kMaxSplit && bh * tiles * p.splits * 2 <= sms && p.splits * 4 <= ktiles) p.splits *= 2;
+  p.row_tiles = (int)(pair ? pairs : tiles);
+  p.items = (int)(bh * p.row_tiles);
+
+  AttnMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  int st_q = heads_map(&maps.q, a->q, a->batch, a->q_tokens, a->heads, a->dim, (uint32_t)p.group,
+                       (uint32_t)p.tok_tile, &p.q_bm, &p.q_hm);
+  const int64_t kt = a->kv_tokens > 0 ? a->kv_tokens : 1;
+  int st_k = heads_map(&maps.k, kh, a->batch, kt, a->kv_heads, a->dim, 1, kKeys, &p.k_bm, &p.k_hm);
+  int st_v = heads_map(&maps.v, vh, a->batch, kt, a->kv_heads, a->dim, 1, kKeys, &p.v_bm, &p.v_hm);
+  if (st_q != SVDQ_OK || st_k != SVDQ_OK || st_v != SVDQ_OK) return SVDQ_ERR_CUDA;
+
+  NvtxRange range("svdq/cross_attn");
+  const cudaStream_t s = (cudaStream_t)stream;
+  const bool wide = p.d > 64;
+  if (pair) {
+    const int grid = p.items < sms ? p.items : sms;
+    return (svdq_status)(wide ? launch<true, 2>(maps, p, dev, grid, s) : launch<true, 1>(maps, p, dev, grid, s));
+  }
+  const int grid = p.items * p.splits;
+  return (svdq_status)(wide ? launch<false, 2>(maps, p, dev, grid, s) : launch<false, 1>(maps, p, dev, grid, s));
+}

@@ -156,6 +156,26 @@ int encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base
   return r == CUDA_SUCCESS ? SVDQ_OK : SVDQ_ERR_CUDA;
 }
 
+int encode_tmap_4d_bf16(CUtensorMap* map, const void* base, const uint64_t dims[4], const uint64_t stride_bytes[3],
+                        const uint32_t box[4]) {
+  auto fn = get_encode();
+  if (!fn) return SVDQ_ERR_CUDA;
+  if ((uintptr_t)base & 15) return SVDQ_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (stride_bytes[i] & 15) return SVDQ_ERR_INVALID_ARG;
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4], estr[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 4; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    if (i < 3) st[i] = stride_bytes[i];
+  }
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, st, bx, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SVDQ_OK : SVDQ_ERR_CUDA;
+}
+
 }  // namespace svdq
 
 using namespace svdq;

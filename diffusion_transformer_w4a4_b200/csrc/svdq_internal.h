@@ -154,6 +154,11 @@ uint8_t int_to_e4m3(int v);
 int encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);
 
+// The same for a bf16 tensor of four dimensions (innermost contiguous; sizes, byte
+// strides of the outer three and box in the order innermost first), 128-byte swizzle.
+int encode_tmap_4d_bf16(CUtensorMap* map, const void* base, const uint64_t dims[4], const uint64_t stride_bytes[3],
+                        const uint32_t box[4]);
+
 unsigned long long wait_limit_cycles();
 int device_sm_count(int dev);  // multiprocessor count, cached per device (148 if the query fails)
 // SVDQ_OK iff `dev` (a layer's device) is the calling thread's current device,
@@ -164,6 +169,11 @@ int require_current_device(int dev);
 // device other than `dev`; SVDQ_OK otherwise (managed memory, or a pointer the
 // runtime cannot classify, is left to the caller).
 int check_blob_pointer(const void* p, int dev);
+
+// A bf16 [batch, tokens, heads, dim] view: SVDQ_OK iff pointer and strides are as svdq.h asks
+// (`out`: no broadcast dimension), and the bytes from its first to its last element.
+int check_heads(const svdq_heads& h, int64_t batch, int64_t tokens, int64_t heads, int64_t dim, bool out);
+int64_t heads_extent(const svdq_heads& h, int64_t batch, int64_t tokens, int64_t heads, int64_t dim);
 
 // Kernel launchers (return svdq_status).
 // dynamic activation scale: grid of the amax pass (its CTA count is the number

@@ -410,6 +410,128 @@ svdq_status svdq_w8a8_forward(const svdq_w8a8_layer* layer, const void* X, int64
 svdq_status svdq_w8a8_read_status(const svdq_w8a8_layer* layer, int64_t M, const void* ws, size_t ws_bytes,
                                   int* device_status);
 
+/* ------------------------------------------------------------------------ */
+/* FP8 linear layer with one scale for each block of 128.                    */
+/* ------------------------------------------------------------------------ */
+/* The 8-bit layer for weights whose range differs from block to block, beside
+ * the tensorwise W8A8 layer:
+ *   weight:     s_w[i,j] for rows 128i.. and inputs 128j.., fixed,
+ *   activation: s_x[m,j] for token m and inputs 128j.., from each input,
+ *   s = fl32(max(max|v|, 2^-100) / 448),  q = E4M3(clamp(fl32(v * fl32(1/s)), +-448)), round half to even,
+ *   Y = bf16( sum_j s_x[m,j] s_w[n/128,j] sum_{k in block j} qx[m,k] qw[n,k] + b[n] ),
+ * products and sums in binary32.  A block whose input holds a NaN or an infinity
+ * gives NaN in that token's outputs.  Shapes: N >= 8 and N % 8 == 0, K >= 16 and
+ * K % 16 == 0 (the last block of either may be short), N <= 2^24, K <= 2^20. */
+typedef struct svdq_fp8_layer svdq_fp8_layer; /* opaque host-side handle */
+
+/* Host, synchronous.  W [N,K] bf16 -> wcodes E4M3 u8 [N,K] (row-major) and
+ * wscales f32 [ceil(N/128), ceil(K/128)].  Errors: INVALID_ARG (shape, pointers),
+ * NUMERIC (non-finite W). */
+svdq_status svdq_fp8_prepare(const uint16_t* W, int64_t N, int64_t K, uint8_t* wcodes, float* wscales);
+
+/* Device layout ("fp8 blob"), regions 1024-byte aligned: bias f32 [N] | wscales
+ * f32 [ceil(N/128), ceil(K/128)] | wcodes u8 [N, K] row-major.  bias bf16 [N] or
+ * NULL (zeros).  wscales may be any finite, non-negative values (a checkpoint's
+ * own); codes other than NaN (0x7F, 0xFF).  Else INVALID_ARG. */
+svdq_status svdq_fp8_packed_size(int64_t N, int64_t K, size_t* bytes);
+svdq_status svdq_fp8_pack(int64_t N, int64_t K, const uint8_t* wcodes, const float* wscales, const uint16_t* bias,
+                          void* blob, size_t blob_bytes);
+
+/* Bind a device-resident fp8 blob (256-byte aligned) to a handle; allocates no
+ * device memory.  UNSUPPORTED_DEVICE on a device other than CC 10.0, INVALID_ARG
+ * for a blob in host memory or on another device. */
+svdq_status svdq_fp8_layer_create(const void* dev_blob, size_t blob_bytes, int64_t N, int64_t K,
+                                  svdq_fp8_layer** out);
+/* Frees the host handle only (never the blob); NULL is a no-op. */
+void svdq_fp8_layer_destroy(svdq_fp8_layer* layer);
+
+/* Workspace for M tokens (caller device memory, 256-byte aligned): activation
+ * codes u8 [M, K] at offset 0 | at the next 1024-byte boundary the activation
+ * scales f32 [ceil(K/128), M'], M' = M rounded up to a multiple of 128 (columns
+ * >= M unused) | at the next 1024-byte boundary int32 status.  Needs no
+ * initialisation: each quantize_act sets the status word to 0. */
+svdq_status svdq_fp8_workspace_size(const svdq_fp8_layer* layer, int64_t M, size_t* bytes);
+
+/* Asynchronous on `stream`; launch errors only.  X [M,K] bf16 and Y [M,N] bf16
+ * are device pointers (16-byte aligned). */
+svdq_status svdq_fp8_quantize_act(const svdq_fp8_layer* layer, const void* X, int64_t M, void* ws, size_t ws_bytes,
+                                  void* stream);
+svdq_status svdq_fp8_gemm(const svdq_fp8_layer* layer, int64_t M, void* Y, void* ws, size_t ws_bytes, void* stream);
+svdq_status svdq_fp8_forward(const svdq_fp8_layer* layer, const void* X, int64_t M, void* Y, void* ws,
+                             size_t ws_bytes, void* stream);
+/* Synchronous read of the workspace status word (SVDQ_ERR_TIMEOUT after a wait
+ * ran past its limit). */
+svdq_status svdq_fp8_read_status(const svdq_fp8_layer* layer, int64_t M, const void* ws, size_t ws_bytes,
+                                 int* device_status);
+
+/* ------------------------------------------------------------------------ */
+/* Between a block's projections: query/key norm with rotation, attention.   */
+/* ------------------------------------------------------------------------ */
+/* The steps of an attention sublayer that the linear layers leave open: the
+ * projections write bf16 [tokens, heads * dim]; the first call normalises and
+ * rotates the queries and keys, the second attends, and its output is the input
+ * of the output projection.
+ *
+ * A bf16 [batch, tokens, heads, dim] view in device memory; dim is contiguous.
+ * Strides in elements, >= 0, multiples of 8 and at least dim (those of
+ * dimensions of size one are ignored); data 16-byte aligned.  A slice of a fused
+ * projection's output is such a view.  Where the text below allows a broadcast,
+ * its stride is 0. */
+typedef struct svdq_heads {
+  void* data;
+  int64_t stride_batch, stride_token, stride_head;
+} svdq_heads;
+
+/* One tensor of svdq_qk_norm_rope. */
+typedef struct svdq_norm_rope_args {
+  svdq_heads x;             /* input (batch and heads may be broadcast) */
+  svdq_heads y;             /* output; y == x (same data and strides) normalises in place, other overlap is an error
+                               that is not detected */
+  int64_t batch, tokens, heads;
+  const void* weight;       /* bf16 [dim], 16-byte aligned, or NULL (ones) */
+  const float* rope;        /* f32 [rope_rows, rot_dim/2, 2]: cosine and sine, 16-byte aligned; NULL: no rotation */
+  int64_t rope_rows;
+  const int32_t* positions; /* i32 [batch, tokens]: the token's row of `rope`; NULL: row = token (rope_rows >= tokens) */
+} svdq_norm_rope_args;
+
+#define SVDQ_PAIRS_INTERLEAVED 0 /* (2i, 2i+1) */
+#define SVDQ_PAIRS_HALVES 1      /* (i, i + rot_dim/2) */
+
+/* y = rotate(weight * x / sqrt(mean x^2 + eps)) for each head of q and k (either
+ * may be NULL), one launch: binary32 throughout, rounded once to bf16.  The
+ * rotation takes the pair (a, c) of the first rot_dim elements of a head to
+ * (a cos - c sin, a sin + c cos) with the token's row of `rope`.  dim % 8 == 0,
+ * 8 <= dim <= 256; rot_dim % 8 == 0, 0 <= rot_dim <= dim (ignored without rope);
+ * eps >= 0.  A position outside [0, rope_rows) reads nothing: the token's heads
+ * become NaN and, if `status` (device int32, may be NULL) is given, it receives
+ * SVDQ_ERR_INVALID_ARG.  Asynchronous on `stream`, on the current device. */
+svdq_status svdq_qk_norm_rope(const svdq_norm_rope_args* q, const svdq_norm_rope_args* k, int64_t dim,
+                              int64_t rot_dim, int pairs, float eps, int32_t* status, void* stream);
+
+typedef struct svdq_attn_args {
+  svdq_heads q;           /* [batch, q_tokens, heads, dim] */
+  svdq_heads k, v;        /* [batch, kv_tokens, kv_heads, dim]; batch and heads may be broadcast */
+  svdq_heads o;           /* [batch, q_tokens, heads, dim], no overlap with the inputs */
+  int64_t batch, q_tokens, kv_tokens, heads, kv_heads, dim;
+  const int32_t* kv_len;  /* i32 [batch]: keys of each sample (clamped to [0, kv_tokens]), or NULL (all) */
+  const uint8_t* kv_mask; /* u8 [batch, kv_tokens], nonzero: the key counts; NULL: all.  Both given: both hold */
+  int64_t mask_stride;    /* elements between the samples' masks (0: one mask for all) */
+  float scale;            /* > 0, finite; usually 1/sqrt(dim) */
+} svdq_attn_args;
+
+/* O[b,s,h,:] = sum_t p_t V[b,t,h',:] / sum_t p_t, p_t = exp(scale * Q[b,s,h,:].K[b,t,h',:]),
+ * over the keys t that count, h' = h / (heads / kv_heads).  Products of bf16 values
+ * with binary32 sums, softmax in binary32; p is rounded to bf16 for the product
+ * with V.  A row without a key (or whose scores are all -inf) gives 0; keys that
+ * do not count have no influence, whatever their K and V hold (NaN included).
+ * dim % 8 == 0, 8 <= dim <= 128; heads % kv_heads == 0, heads <= 4096; token and
+ * batch counts up to 2^30 (batch * heads * ceil(q_tokens / 128) <= 2^30).  kv_tokens may
+ * be 0 (k and v are then not read).  `status` is a device int32, zeroed once by the
+ * caller: an in-kernel wait past its limit records SVDQ_ERR_TIMEOUT there.  No
+ * workspace; equal calls give equal bits.  Asynchronous on `stream`, on the current
+ * device, whose memory every pointer must be. */
+svdq_status svdq_cross_attn(const svdq_attn_args* args, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
