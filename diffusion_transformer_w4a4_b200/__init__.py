@@ -197,6 +197,24 @@ def _stream(stream) -> int | None:
     return int(getattr(stream, "cuda_stream", stream))
 
 
+def _stream_of(stream, device) -> int | None:
+    """_stream for a known device: the raw handle of its current stream, without a Stream object (about 3 us less)."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
+
+
+_torch_module = None
+
+
+def _torch():
+    """torch, imported at the first use (this module loads without it)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
+
+
 # ----------------------------------------------------------------------------- C names
 def svdq_status_string(status: int) -> str:
     return lib().svdq_status_string(int(status)).decode()
@@ -778,18 +796,17 @@ class Fp8Linear:
         return self._ws[M]
 
     def forward(self, x, out=None, stream=None):
-        import torch
-
+        torch = _torch()
         _check_input(x, self.K, self.device)
         M = x.numel() // self.K
         if out is None:
-            out = x.new_empty(M, self.N)
+            out = torch.empty(M, self.N, dtype=torch.bfloat16, device=self.device)
         elif not (out.dtype == torch.bfloat16 and out.device == self.device and out.is_contiguous()
                   and out.numel() == M * self.N):
             raise ValueError(f"expected a contiguous bf16 output [{M}, {self.N}] on {self.device}")
         ws = self.workspace(M)
         with _on(self.device):
-            svdq_fp8_forward(self.handle, x, M, out, ws, stream)
+            svdq_fp8_forward(self.handle, x, M, out, ws, _stream_of(stream, self.device))
         return out
 
     __call__ = forward
@@ -817,20 +834,19 @@ _ROPE_ARGS = struct.Struct("P3qP3q3qPPqP")  # svdq_norm_rope_args
 _ATTN_ARGS = struct.Struct("P3qP3qP3qP3q6qPPqf4x")  # svdq_attn_args
 PAIRS = {"interleaved": 0, "halves": 1}
 _attn_status = {}
+_NO_CONTEXT = contextlib.nullcontext()
 
 
 def _on(device):
     """A context with `device` current (nothing to do, and nothing spent, where it is already)."""
-    import torch
-
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    cuda = _torch().cuda
+    return _NO_CONTEXT if cuda.current_device() == device.index else cuda.device(device)
 
 
 def attn_status(device=None):
     """The status word (int32 tensor of one element) that svdq_cross_attn and svdq_qk_norm_rope report to on
     `device`, unless they are given another: 0, or the code of the first device-side failure (sticky)."""
-    import torch
-
+    torch = _torch()
     device = _layer_device(device)
     t = _attn_status.get(device.index)
     if t is None:
@@ -843,36 +859,30 @@ def attn_status(device=None):
     return t
 
 
-def _check_heads(name, t, device=None):
-    import torch
+def _status_ptr(status, device):
+    if status is None:
+        t = _attn_status.get(device.index)
+        return (attn_status(device) if t is None else t).data_ptr()
+    _check_aux("status", status, _torch().int32, (1,), device)
+    return status.data_ptr()
 
-    if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_cuda:
+
+def _heads(name, t, device):
+    """(pointer, strides of batch, tokens and heads) of a bf16 [batch, tokens, heads, dim] view on `device`."""
+    if t.dtype is not _torch().bfloat16 or t.dim() != 4 or not t.is_cuda:
         raise ValueError(f"{name}: expected a bf16 CUDA tensor [batch, tokens, heads, dim], got {t.dtype} {tuple(t.shape)}")
-    if device is not None and t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} on {t.device}, q on {device}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    sb, st, sh, sd = t.stride()
+    if sd != 1 and t.shape[3] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), sb, st, sh
 
 
 def _check_aux(name, t, dtype, shape, device):
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
-
-
-def _rope_args(name, x, y, weight, rope, positions, device):
-    import torch
-
-    b, s, h, d = x.shape
-    if y.shape != x.shape:
-        raise ValueError(f"{name}: output shape {tuple(y.shape)} for input {tuple(x.shape)}")
-    if weight is not None:
-        _check_aux(f"{name}_weight", weight, torch.bfloat16, (d,), device)
-    if positions is not None:
-        _check_aux("positions", positions, torch.int32, (b, s), device)
-    return _ROPE_ARGS.pack(x.data_ptr(), *x.stride()[:3], y.data_ptr(), *y.stride()[:3], b, s, h,
-                           0 if weight is None else weight.data_ptr(), 0 if rope is None else rope.data_ptr(),
-                           0 if rope is None else rope.shape[0], 0 if positions is None else positions.data_ptr())
 
 
 def svdq_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, *, eps=1e-6, rope=None, positions=None,
@@ -882,43 +892,49 @@ def svdq_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, *, eps=1e-6, rope
     "interleaved" or "halves"): row positions[b, s] (int32 [B,S]), or row s without positions.  Any strided view
     with contiguous heads (a slice of a fused projection's output); out_q / out_k may be q / k themselves.  Returns
     the rotated q, or (q, k)."""
-    import torch
-
-    _check_heads("q", q)
+    torch = _torch()
     device = q.device
-    rot = 0
+    table = rows = pos = rot = 0
     if rope is not None:
         if rope.dim() != 3 or rope.shape[2] != 2:
             raise ValueError(f"rope: expected [rows, rot/2, 2], got {tuple(rope.shape)}")
         _check_aux("rope", rope, torch.float32, rope.shape, device)
-        rot = 2 * rope.shape[1]
+        rows, half, _ = rope.shape
+        table, rot = rope.data_ptr(), 2 * half
     elif positions is not None:
         raise ValueError("positions need a rope table")
-    if out_q is None:
-        out_q = q.new_empty(q.shape)
-    else:
-        _check_heads("out_q", out_q, device)
-    qa = _rope_args("q", q, out_q, q_weight, rope, positions, device)
-    ka = None
-    if k is not None:
-        _check_heads("k", k, device)
-        if k.shape[3] != q.shape[3]:
-            raise ValueError(f"heads of {q.shape[3]} (q) and {k.shape[3]} (k)")
-        if out_k is None:
-            out_k = k.new_empty(k.shape)
+    packed = [None, None]
+    outs = [out_q, out_k]
+    for i, (name, x, w) in enumerate((("q", q, q_weight), ("k", k, k_weight))):
+        if x is None:
+            continue
+        xa = _heads(name, x, device)
+        shape = x.shape
+        b, s, h, d = shape
+        if outs[i] is None:
+            outs[i] = torch.empty_like(x)
+            ya = outs[i].data_ptr(), *outs[i].stride()[:3]
         else:
-            _check_heads("out_k", out_k, device)
-        ka = _rope_args("k", k, out_k, k_weight, rope, positions, device)
-    if status is None:
-        status = _attn_status.get(device.index)
-        if status is None:
-            status = attn_status(device)
-    else:
-        _check_aux("status", status, torch.int32, (1,), device)
+            ya = _heads("out_" + name, outs[i], device)
+            if outs[i].shape != shape:
+                raise ValueError(f"out_{name}: {tuple(outs[i].shape)} for {tuple(shape)}")
+        wp = 0
+        if w is not None:
+            _check_aux(name + "_weight", w, torch.bfloat16, (d,), device)
+            wp = w.data_ptr()
+        if positions is not None:
+            if i == 0:
+                _check_aux("positions", positions, torch.int32, (b, s), device)
+                pos = positions.data_ptr()
+            elif positions.shape != (b, s):
+                raise ValueError(f"positions {tuple(positions.shape)} for k {tuple(shape)}")
+        if i == 1 and d != q.shape[3]:
+            raise ValueError(f"heads of {q.shape[3]} (q) and {d} (k)")
+        packed[i] = _ROPE_ARGS.pack(*xa, *ya, b, s, h, wp, table, rows, pos)
     with _on(device):
-        _check(lib().svdq_qk_norm_rope(qa, ka, q.shape[3], rot, PAIRS[pairs], eps, status.data_ptr(), _stream(stream)),
-               "svdq_qk_norm_rope")
-    return out_q if k is None else (out_q, out_k)
+        _check(lib().svdq_qk_norm_rope(packed[0], packed[1], q.shape[3], rot, PAIRS[pairs], eps,
+                                       _status_ptr(status, device), _stream_of(stream, device)), "svdq_qk_norm_rope")
+    return outs[0] if k is None else (outs[0], outs[1])
 
 
 def svdq_cross_attn(q, k, v, *, kv_len=None, kv_mask=None, scale=None, out=None, status=None, stream=None):
@@ -926,41 +942,33 @@ def svdq_cross_attn(q, k, v, *, kv_len=None, kv_mask=None, scale=None, out=None,
     and heads of k and v may be expanded): softmax(scale q k^T) v over the first kv_len[b] keys (int32 [B]) with
     kv_mask[b, t] nonzero (uint8 or bool [B,Sk]).  Rows without a key give 0.  scale defaults to 1/sqrt(D).
     Returns bf16 [B,Sq,H,D]."""
-    import torch
-
-    _check_heads("q", q)
+    torch = _torch()
     device = q.device
-    _check_heads("k", k, device)
-    _check_heads("v", v, device)
-    b, sq, h, d = q.shape
-    _, sk, hk, _ = k.shape
-    if k.shape != v.shape or k.shape[0] != b or k.shape[3] != d:
-        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)} do not fit")
+    qa, ka, va = _heads("q", q, device), _heads("k", k, device), _heads("v", v, device)
+    shape, ks = q.shape, k.shape
+    b, sq, h, d = shape
+    kb, sk, hk, kd = ks
+    if ks != v.shape or kb != b or kd != d:
+        raise ValueError(f"q {tuple(shape)}, k {tuple(ks)}, v {tuple(v.shape)} do not fit")
     if out is None:
-        out = q.new_empty(q.shape)
+        out = torch.empty_like(q)
+        oa = out.data_ptr(), *out.stride()[:3]
     else:
-        _check_heads("out", out, device)
-        if out.shape != q.shape:
-            raise ValueError(f"out {tuple(out.shape)} for q {tuple(q.shape)}")
+        oa = _heads("out", out, device)
+        if out.shape != shape:
+            raise ValueError(f"out {tuple(out.shape)} for q {tuple(shape)}")
+    lens = mask = mask_ld = 0
     if kv_len is not None:
         _check_aux("kv_len", kv_len, torch.int32, (b,), device)
-    mask, mask_ld = 0, 0
+        lens = kv_len.data_ptr()
     if kv_mask is not None:
-        if kv_mask.dtype not in (torch.uint8, torch.bool) or kv_mask.device != device or \
-                tuple(kv_mask.shape) != (b, sk) or (sk > 1 and kv_mask.stride(1) != 1):
+        if kv_mask.dtype not in (torch.uint8, torch.bool) or kv_mask.device != device or kv_mask.shape != (b, sk) or \
+                (sk > 1 and kv_mask.stride(1) != 1):
             raise ValueError(f"kv_mask: expected uint8 or bool [{b}, {sk}] on {device}, rows contiguous, got "
                              f"{kv_mask.dtype} {tuple(kv_mask.shape)} on {kv_mask.device}")
         mask, mask_ld = kv_mask.data_ptr(), kv_mask.stride(0)
-    if status is None:
-        status = _attn_status.get(device.index)
-        if status is None:
-            status = attn_status(device)
-    else:
-        _check_aux("status", status, torch.int32, (1,), device)
-    args = _ATTN_ARGS.pack(q.data_ptr(), *q.stride()[:3], k.data_ptr(), *k.stride()[:3], v.data_ptr(),
-                           *v.stride()[:3], out.data_ptr(), *out.stride()[:3], b, sq, sk, h, hk, d,
-                           0 if kv_len is None else kv_len.data_ptr(), mask, mask_ld,
+    args = _ATTN_ARGS.pack(*qa, *ka, *va, *oa, b, sq, sk, h, hk, d, lens, mask, mask_ld,
                            d ** -0.5 if scale is None else scale)
     with _on(device):
-        _check(lib().svdq_cross_attn(args, status.data_ptr(), _stream(stream)), "svdq_cross_attn")
+        _check(lib().svdq_cross_attn(args, _status_ptr(status, device), _stream_of(stream, device)), "svdq_cross_attn")
     return out

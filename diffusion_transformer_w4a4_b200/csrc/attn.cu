@@ -102,6 +102,18 @@ __device__ __forceinline__ void key_words(const AttnParams& p, int b, int t, int
   }
 }
 
+// 16 outputs of a row from column `col` on (those below dim), at element `at`; wide: whole 32-byte sectors.
+__device__ __forceinline__ void store_16(const AttnParams& p, long long at, int col, bool wide, const uint32_t (&y)[8]) {
+  if (wide) {
+    if (col < p.d && SVDQ_INB(p.status, 2 * at, 32, p.out_extent)) st_global_32b(p.out + at, y);
+  } else {
+    if (col < p.d && SVDQ_INB(p.status, 2 * at, 16, p.out_extent))
+      *(uint4*)(p.out + at) = make_uint4(y[0], y[1], y[2], y[3]);
+    if (col + 8 < p.d && SVDQ_INB(p.status, 2 * at + 16, 16, p.out_extent))
+      *(uint4*)(p.out + at + 8) = make_uint4(y[4], y[5], y[6], y[7]);
+  }
+}
+
 // One work item: sample, item head, first token of stream 0, key tiles.
 struct Item {
   int b, h, tok0, nkeys, t0, t1;
@@ -154,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
   uint64_t* mma_done = o_full + 2;
   uint32_t* tmem_slot = (uint32_t*)(mma_done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   WaitCtl wc{abort_flag, p.status, p.limit};
 
   if (threadIdx.x == 0) {
@@ -201,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
       bool ok = true;
       auto load_kv = [&](const CUtensorMap* map, int head, int bat, int t) {
         const int s = pos % SLOTS;
-        if (!mbar_wait(&kv_empty[s], ((pos / SLOTS) & 1) ^ 1, wc)) return false;
+        if (!timed_wait(&kv_empty[s], ((pos / SLOTS) & 1) ^ 1, wc)) return false;
         mbar_arrive_expect_tx(&kv_full[s], G::kTile);
 #pragma unroll
         for (int ch = 0; ch < DC; ++ch)
@@ -216,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         if (n == 0) continue;
         const int kvh = (int)((long long)it.h * p.group * p.hk / p.hq);
         for (int s = 0; s < (it.second ? 2 : 1) && ok; ++s) {
-          if (!mbar_wait(&q_empty[s], (nq[s] & 1) ^ 1, wc)) {
+          if (!timed_wait(&q_empty[s], (nq[s] & 1) ^ 1, wc)) {
             ok = false;
             break;
           }
@@ -238,43 +250,48 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
           }
         }
       }
-      if (!ok) {  // drain copies still in flight
-        for (int j = (pos > SLOTS ? pos - SLOTS : 0); j < pos; ++j)
-          mbar_wait_drain(&kv_full[j % SLOTS], (j / SLOTS) & 1, p.limit);
-        for (int s = 0; s < 2; ++s)
-          if (nq[s]) mbar_wait_drain(&q_full[s], (nq[s] - 1) & 1, p.limit);
-      }
+      // No block leaves with copies in flight, whoever gave up on them.
+      for (int j = (pos > SLOTS ? pos - SLOTS : 0); j < pos; ++j)
+        mbar_wait_drain(&kv_full[j % SLOTS], (j / SLOTS) & 1, drain_limit(p.limit));
+      for (int s = 0; s < 2; ++s)
+        if (nq[s]) mbar_wait_drain(&q_full[s], (nq[s] - 1) & 1, drain_limit(p.limit));
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
+    if (elect_one()) {
+      // An instruction keeps the tensor cores busy for 64 clocks, so issuing one has to cost less: descriptors are
+      // one addition each.
+      constexpr uint64_t kDescK = sdesc_const(16, 1024, LAYOUT_SW128), kDescV = sdesc_const(kChunkBytes, 1024, LAYOUT_SW128);
+      const uint64_t q_desc = kDescK + sdesc_addr(sm_q), k_desc = kDescK + sdesc_addr(sm_kv);
+      const uint64_t v_desc = kDescV + sdesc_addr(sm_kv);
       const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
       const uint32_t idesc_o = idesc_bf16_f32(kRows, p.npv) | (1u << 16);  // B (= V) has the head dimension contiguous
       int base = 0, fixes = 0;
       int nq[2] = {0, 0}, np[2] = {0, 0};
       bool ok = true;
       auto slot_wait = [&](int pos) {
-        if (!mbar_wait(&kv_full[pos % SLOTS], (pos / SLOTS) & 1, wc)) return false;
+        if (!timed_wait(&kv_full[pos % SLOTS], (pos / SLOTS) & 1, wc)) return false;
         tc_fence_after();
         return true;
       };
       auto issue_s = [&](int s, int pos) {
-        const uint32_t qa = smem_u32(sm_q + (PAIR ? s : 0) * G::kTile);
-        const uint32_t ka = smem_u32(sm_kv + (pos % SLOTS) * G::kTile);
-        for (int kk = 0; kk < p.ksteps; ++kk) {
-          const uint32_t off = (uint32_t)((kk >> 2) * kChunkBytes + (kk & 3) * 32);
-          mma_bf16(tmem + s * 128, make_sdesc(qa + off, 16, 1024, LAYOUT_SW128),
-                   make_sdesc(ka + off, 16, 1024, LAYOUT_SW128), idesc_s, kk != 0 ? 1u : 0u);
+        const uint64_t qd = q_desc + (uint32_t)((PAIR ? s : 0) * (G::kTile >> 4));
+        const uint64_t kd = k_desc + (uint32_t)((pos % SLOTS) * (G::kTile >> 4));
+        const uint32_t d = tmem + s * 128;
+#pragma unroll
+        for (int kk = 0; kk < 4 * DC; ++kk) {
+          if (kk >= p.ksteps) break;
+          const uint32_t off = (uint32_t)(((kk >> 2) * kChunkBytes + (kk & 3) * 32) >> 4);
+          mma_bf16(d, qd + off, kd + off, idesc_s, kk != 0 ? 1u : 0u);
         }
         umma_commit(&s_full[s]);
       };
       auto issue_o = [&](int s, int pos, bool first) {
-        const uint32_t va = smem_u32(sm_kv + (pos % SLOTS) * G::kTile);
+        const uint64_t vd = v_desc + (uint32_t)((pos % SLOTS) * (G::kTile >> 4));
+        const uint32_t d = tmem + 256 + s * 128, pa = tmem + s * 128;
+        mma_bf16_ts(d, pa, vd, idesc_o, first ? 0u : 1u);
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_bf16_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * kk,
-                      make_sdesc(va + 2048 * kk, kChunkBytes, 1024, LAYOUT_SW128), idesc_o,
-                      (first && kk == 0) ? 0u : 1u);
+        for (int kk = 1; kk < kKeys / 16; ++kk) mma_bf16_ts(d, pa + 8 * kk, vd + 128 * kk, idesc_o, 1u);
       };
       for (int item = item0; item < p.items && ok; item += item_step) {
         const Item it = item_of<PAIR>(p, item, split);
@@ -285,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         for (int s = 0; s < 2 && ok; ++s) {
           if (!has(0, s)) continue;
           if (PAIR || s == 0) {
-            ok = mbar_wait(&q_full[s], nq[s] & 1, wc);
+            ok = timed_wait(&q_full[s], nq[s] & 1, wc);
             ++nq[s];
           }
           const int kp = base + ring_pos<PAIR>(0, s, false, n);
@@ -303,11 +320,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
             if (!PAIR || s == 0) {
               ok = slot_wait(vp);
               if (ok && fixing) {
-                ok = mbar_wait(&v_fixed[fixes % SLOTS], (fixes / SLOTS) & 1, wc);
+                ok = timed_wait(&v_fixed[fixes % SLOTS], (fixes / SLOTS) & 1, wc);
                 ++fixes;
               }
             }
-            ok = ok && mbar_wait(&p_full[s], np[s] & 1, wc);
+            ok = ok && timed_wait(&p_full[s], np[s] & 1, wc);
             if (!ok) break;
             ++np[s];
             tc_fence_after();
@@ -330,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         base += 2 * n;
       }
       umma_commit(mma_done);
-      mbar_wait_drain(mma_done, 0, p.limit);
+      mbar_wait_drain(mma_done, 0, drain_limit(p.limit));
     }
   } else if (warp == 10) {
     // ------------------------------------------------------------ zero the masked rows of V
@@ -346,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         uint32_t w[4];
         key_words(p, it.b, t, it.nkeys, lane, w);
         const int pos = base + (PAIR ? ring_pos<PAIR>(j, 0, true, n) : ring_pos<PAIR>(j >> 1, j & 1, true, n));
-        ok = warp_wait(&kv_full[pos % SLOTS], (pos / SLOTS) & 1, wc);
+        ok = warp_timed_wait(&kv_full[pos % SLOTS], (pos / SLOTS) & 1, wc);
         if (!ok) break;
         uint8_t* tile = sm_kv + (pos % SLOTS) * G::kTile;
 #pragma unroll
@@ -395,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         const bool masked = p.kv_mask || it.nkeys < (t + 1) * kKeys;
         uint32_t w[4] = {0, 0, 0, 0};
         if (masked) key_words(p, it.b, t, it.nkeys, lane, w);
-        ok = warp_wait(&s_full[st], ns & 1, wc);
+        ok = warp_timed_wait(&s_full[st], ns & 1, wc);
         if (!ok) break;
         ++ns;
         tc_fence_after();
@@ -403,20 +420,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
           uint32_t sr[4][32];
 #pragma unroll
           for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(t_s + 32 * k, sr[k]);
+          tmem_ld_wait_regs(sr[0]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld_wait_regs(sr[k]);
+          for (int k = 1; k < 4; ++k) reg_order(sr[k]);
           if (masked) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                sr[k][j] = (w[k] >> j) & 1u ? sr[k][j] : 0xFF800000u;  // -inf
+              for (int j = 0; j < 32; ++j) sr[k][j] = (w[k] >> j) & 1u ? sr[k][j] : 0xFF800000u;  // -inf
           }
-          float mx = m;
+          float m4[4] = {m, m, m, m};  // four chains
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int j = 0; j < 32; j += 2)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(sr[k][j]));
+            for (int k = 0; k < 4; ++k)
+              m4[k] = fmaxf(fmaxf(m4[k], __uint_as_float(sr[k][j])), __uint_as_float(sr[k][j + 1]));
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           if (i == 0) {
             m = mx;
           } else if (__any_sync(0xffffffffu, (mx - m) * p.c > kLazy)) {
@@ -427,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
             for (int cc = 0; cc < p.npv; cc += 16) {
               uint32_t o[16];
               tmem_ld_32x32b_x16(t_o + cc, o);
-              tmem_ld_wait();
+              tmem_ld_wait_regs(o);
 #pragma unroll
               for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
               tmem_st_32x32b_x16(t_o + cc, o);
@@ -440,9 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
             uint32_t pr[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const uint32_t(&src)[32] = sr[k + (j >> 4)];
-              const float e0 = ex2(fmaf(__uint_as_float(src[2 * (j & 15)]), p.c, -mc));
-              const float e1 = ex2(fmaf(__uint_as_float(src[2 * (j & 15) + 1]), p.c, -mc));
+              const float e0 = ex2(fmaf(__uint_as_float(sr[k + (j >> 4)][2 * (j & 15)]), p.c, -mc));
+              const float e1 = ex2(fmaf(__uint_as_float(sr[k + (j >> 4)][2 * (j & 15) + 1]), p.c, -mc));
               l4[j & 3] += e0 + e1;
               __nv_bfloat162 hv = __floats2bfloat162_rn(e0, e1);
               pr[j] = *(uint32_t*)&hv;
@@ -459,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
       if (PAIR) {
         if (!ok) break;
         if (n > 0) {
-          ok = warp_wait(&o_full[st], no & 1, wc);
+          ok = warp_timed_wait(&o_full[st], no & 1, wc);
           if (!ok) break;
           ++no;
           tc_fence_after();
@@ -468,28 +486,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
           const float inv = l == 0.f ? 0.f : 1.f / l;  // a row without a key: 0
           const long long off = (long long)it.b * p.o_sb + (long long)tok * p.o_st +
                                 (long long)(it.h * p.group + r_head) * p.o_sh;
-          for (int cc = 0; cc < p.npv; cc += 16) {
-            uint32_t o[16];
+          const bool wide = ((p.o_sb | p.o_st | p.o_sh) & 15) == 0 && ((uintptr_t)p.out & 31) == 0 && (p.d & 15) == 0;
+          for (int cc = 0; cc < p.npv; cc += 32) {
+            uint32_t o[32];
             if (n > 0) {
-              tmem_ld_32x32b_x16(t_o + cc, o);
-              tmem_ld_wait();
+              tmem_ld_32(t_o + cc, o);
             } else {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = 0;
+              for (int j = 0; j < 32; ++j) o[j] = 0;
             }
-            uint32_t y[8];
+            uint32_t y[2][8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 16; ++j) {
               __nv_bfloat162 hv = l == 0.f ? __floats2bfloat162_rn(0.f, 0.f)
                                            : __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv,
                                                                    __uint_as_float(o[2 * j + 1]) * inv);
-              y[j] = *(uint32_t*)&hv;
+              y[j >> 3][j & 7] = *(uint32_t*)&hv;
             }
             if (valid) {
 #pragma unroll
-              for (int v = 0; v < 2; ++v)
-                if (cc + 8 * v < p.d && SVDQ_INB(p.status, 2 * (off + cc + 8 * v), 16, p.out_extent))
-                  *(uint4*)(p.out + off + cc + 8 * v) = make_uint4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
+              for (int v = 0; v < 2; ++v) store_16(p, off + cc + 16 * v, cc + 16 * v, wide, y[v]);
             }
           }
           tc_fence_before();  // these loads come before the products that the next P lets start
@@ -499,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         sm_m[st * 128 + row] = m;
         sm_l[st * 128 + row] = l;
         for (int s = 0; s < 2 && ok; ++s)
-          if (s < n) ok = warp_wait(&o_full[s], 0, wc);
+          if (s < n) ok = warp_timed_wait(&o_full[s], 0, wc);
         ok = named_bar_and(1, 256, ok);
         if (!ok) break;
         tc_fence_after();
@@ -519,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
             for (int j = 0; j < 16; ++j) a[j] = b[j] = 0;
             if (n > 0) tmem_ld_32x32b_x16(tmem + lanes + 256 + cc, a);
             if (n > 1) tmem_ld_32x32b_x16(tmem + lanes + 384 + cc, b);
-            tmem_ld_wait();
+            tmem_ld_wait_regs(a);
+            tmem_ld_wait_regs(b);
             float o[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = fmaf(__uint_as_float(a[j]), f0, __uint_as_float(b[j]) * f1);

@@ -29,7 +29,7 @@ struct svdq_fp8_layer {
   const float* bias;     // [N]
   const float* wscales;  // [NB, KB]
   const uint8_t* wcodes;  // [N, K]
-  CUtensorMap map_w[3];  // boxes of 256, 128 and 64 rows
+  CUtensorMap map_w[3];  // boxes of 96, 128 and 64 rows
 };
 
 namespace svdq {
@@ -117,17 +117,25 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp8_quantize(const uint16_t* 
 }
 
 // ------------------------------------------------------------------ GEMM
-template <int BN>
+// PAIR: two CTAs on a 256 x 192 tile (each 128 rows of X and 96 of W a stage, 128 x 192 of the sums).  One CTA
+// alone on 128 x 192 would read 40 KiB for 384 clocks of products, 104 bytes a clock, which the L2 does not give to
+// 148 SMs at once; a pair reads 28 KiB a CTA.
+// A fold costs a warp about three times a tensor-memory latency whatever its width, so a tile's columns go to
+// warpgroups of 64 columns each: 64 sums and 64 loaded columns a thread, three warps to each scheduler at 192.
+template <int BN, bool PAIR>
 struct Tile {
-  static constexpr int kStageA = 128 * kBlk, kStageB = BN * kBlk, kStage = kStageA + kStageB;
-  static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
-  static constexpr int kBufs = BN == 256 ? 2 : 4;  // tensor-memory accumulators in flight
-  static constexpr uint32_t kCols = BN * kBufs;
+  static constexpr int kRowsB = PAIR ? BN / 2 : BN;  // rows of W in this CTA's stage
+  static constexpr int kStageA = 128 * kBlk, kStageB = kRowsB * kBlk, kStage = kStageA + kStageB;
+  static constexpr int kStages = BN == 192 ? 7 : (BN == 128 ? 6 : 8);
+  static constexpr int kBufs = BN == 192 ? 2 : 4;  // tensor-memory accumulators in flight
+  static constexpr uint32_t kCols = BN == 192 ? 512 : BN * kBufs;
+  static constexpr int kTileM = PAIR ? 256 : 128;
+  static constexpr int kFoldWarps = BN / 16;  // warps 0.. fold (a warpgroup for 64 columns)
+  static constexpr int kLoadWarp = kFoldWarps, kMmaWarp = kFoldWarps + 1;
+  static constexpr int kThreads = 32 * kFoldWarps + 128;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
-constexpr int kEpiWarp0 = 2, kEpiWarps = 8;
-constexpr int kGemmThreads = (kEpiWarp0 + kEpiWarps) * 32;
 
 struct F8Params {
   int M, N, KB, NB, m_tiles, num_tiles;
@@ -143,11 +151,10 @@ struct F8Maps {
   CUtensorMap a, b;
 };
 
-template <int BN>
-__global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_constant__ F8Maps maps,
+template <int BN, bool PAIR>
+__global__ void __launch_bounds__((Tile<BN, PAIR>::kThreads), 1) k_gemm_fp8(const __grid_constant__ F8Maps maps,
                                                              const __grid_constant__ F8Params p) {
-  using T = Tile<BN>;
-  constexpr int HALF = BN / 2;
+  using T = Tile<BN, PAIR>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* stages = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);  // [kStages][A | B]
   uint64_t* full = (uint64_t*)(stages + T::kStages * T::kStage);
@@ -157,17 +164,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
   uint64_t* mma_done = acc_empty + T::kBufs;
   uint32_t* tmem_slot = (uint32_t*)(mma_done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   WaitCtl wc{abort_flag, p.status, p.limit};
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0;  // the CTA of rank 0 issues the pair's products
+  const int tile0 = PAIR ? blockIdx.x >> 1 : blockIdx.x, tile_step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], PAIR && rank == 0 ? 2 : 1);  // rank 0 also waits for the other CTA's stage
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < T::kBufs; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], kEpiWarps);
+      mbar_init(&acc_empty[b], (PAIR ? 2 : 1) * T::kFoldWarps);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
@@ -176,128 +185,202 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
   // The quantizer's codes and scales; and an earlier kernel that let this one start may still need tensor
   // memory on this SM, so the allocation comes behind it too.
   pdl_wait();
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, T::kCols);
-    tmem_relinquish();
+  if (warp == T::kMmaWarp) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, T::kCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, T::kCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // both CTAs' barriers and tensor memory are there
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
+  if (warp >= T::kFoldWarps) {
+    if (warp == T::kLoadWarp && lane == 0) {
+      // ---------------------------------------------------------- TMA producer
       prefetch_tmap(&maps.a);
       prefetch_tmap(&maps.b);
       int it = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < p.num_tiles && ok; tile += gridDim.x) {
+      for (int tile = tile0; tile < p.num_tiles && ok; tile += tile_step) {
         const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
         for (int j = 0; j < p.KB; ++j, ++it) {
           const int s = it % T::kStages;
-          if (!mbar_wait(&empty[s], ((it / T::kStages) & 1) ^ 1, wc)) {
+          if (!timed_wait(&empty[s], ((it / T::kStages) & 1) ^ 1, wc)) {
             ok = false;
             break;
           }
           uint8_t* st = stages + s * T::kStage;
           mbar_arrive_expect_tx(&full[s], T::kStage);
-          tma_load_2d(&maps.a, &full[s], st, j * kBlk, mt * 128);
-          tma_load_2d(&maps.b, &full[s], st + T::kStageA, j * kBlk, nt * BN);
+          tma_load_2d(&maps.a, &full[s], st, j * kBlk, mt * T::kTileM + (int)rank * 128);
+          tma_load_2d(&maps.b, &full[s], st + T::kStageA, j * kBlk, nt * BN + (int)rank * T::kRowsB);
         }
       }
-      if (!ok) {  // drain copies still in flight
-        for (int j = (it > T::kStages ? it - T::kStages : 0); j < it; ++j)
-          mbar_wait_drain(&full[j % T::kStages], (j / T::kStages) & 1, p.limit);
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer: one accumulator per block of 128
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < p.num_tiles && ok; tile += gridDim.x) {
-        for (int j = 0; j < p.KB; ++j, ++it) {
-          const int s = it % T::kStages, b = it % T::kBufs;
-          if (!mbar_wait(&acc_empty[b], ((it / T::kBufs) & 1) ^ 1, wc) ||
-              !mbar_wait(&full[s], (it / T::kStages) & 1, wc)) {
-            ok = false;
-            break;
+      // No block leaves with copies in flight, whoever gave up on them.
+      for (int j = (it > T::kStages ? it - T::kStages : 0); j < it; ++j)
+        mbar_wait_drain(&full[j % T::kStages], (j / T::kStages) & 1, drain_limit(p.limit));
+    } else if (PAIR && rank == 1 && warp == T::kMmaWarp) {
+      // ---------------------------------------------------------- the pair's other CTA: pass on that a stage is loaded
+      if (lane == 0) {
+        int it = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < p.num_tiles && ok; tile += tile_step)
+          for (int j = 0; j < p.KB && ok; ++j, ++it) {
+            const int s = it % T::kStages;
+            ok = timed_wait(&full[s], (it / T::kStages) & 1, wc);
+            if (ok) mbar_arrive_cluster(dsmem_addr(smem_u32(&full[s]), 0));
           }
+      }
+    } else if (warp == T::kMmaWarp) {
+      // ---------------------------------------------------------- MMA issuer: one accumulator per block of 128
+      // The whole warp walks the loop (its values then live in uniform registers, where the instruction wants
+      // them) and one lane issues.
+      constexpr uint64_t kDesc = sdesc_const(16, 1024, LAYOUT_SW128);
+      constexpr uint32_t idesc = idesc_e4m3_f32(PAIR ? 256 : 128, BN);
+      const uint32_t first = sdesc_addr(stages);
+      int s = 0, b = 0;
+      uint32_t s_par = 0, b_par = 1;
+      bool ok = true;
+      for (int tile = tile0; tile < p.num_tiles && ok; tile += tile_step) {
+        for (int j = 0; j < p.KB; ++j) {
+          ok = warp_timed_wait(&acc_empty[b], b_par, wc) && warp_timed_wait(&full[s], s_par, wc);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(stages + s * T::kStage), b_addr = a_addr + T::kStageA;
+          const uint64_t da = kDesc + first + (uint32_t)(s * (T::kStage >> 4)), db = da + (T::kStageA >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < kBlk / 32; ++kk)  // K = 32 codes (bytes) per instruction
-            mma_f8f6f4(tmem + b * BN, make_sdesc(a_addr + 32 * kk, 16, 1024, LAYOUT_SW128),
-                       make_sdesc(b_addr + 32 * kk, 16, 1024, LAYOUT_SW128), idesc_e4m3_f32(128, BN), kk != 0 ? 1u : 0u);
-          umma_commit(&empty[s]);
-          umma_commit(&acc_full[b]);
+            for (int kk = 0; kk < kBlk / 32; ++kk) {  // K = 32 codes (bytes) per instruction
+              if constexpr (PAIR)
+                mma_f8f6f4_pair(tmem + b * BN, da + 2 * kk, db + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+              else
+                mma_f8f6f4(tmem + b * BN, da + 2 * kk, db + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+            }
+            if constexpr (PAIR) {
+              umma_commit_both(&empty[s]);
+              umma_commit_both(&acc_full[b]);
+            } else {
+              umma_commit(&empty[s]);
+              umma_commit(&acc_full[b]);
+            }
+          }
+          __syncwarp();
+          if (++s == T::kStages) {
+            s = 0;
+            s_par ^= 1;
+          }
+          if (++b == T::kBufs) {
+            b = 0;
+            b_par ^= 1;
+          }
         }
       }
-      umma_commit(mma_done);
-      mbar_wait_drain(mma_done, 0, p.limit);
+      if (elect_one()) {
+        if constexpr (PAIR)
+          umma_commit_pair(mma_done);
+        else
+          umma_commit(mma_done);
+        mbar_wait_drain(mma_done, 0, drain_limit(p.limit));
+      }
+      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ fold and epilogue
-    const int q = warp & 3;                 // tensor-memory lane quarter
-    const int h = (warp - kEpiWarp0) >> 2;  // column half
+    const int q = warp & 3;   // tensor-memory lane quarter
+    const int h = warp >> 2;  // columns 64 h.. of the tile: inside one block of 128 rows of W
     int it = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < p.num_tiles && ok; tile += gridDim.x) {
+    for (int tile = tile0; tile < p.num_tiles && ok; tile += tile_step) {
       const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
-      const int m = mt * 128 + 32 * q + lane;
-      const int n0 = nt * BN + h * HALF;
+      const int m = mt * T::kTileM + (int)rank * 128 + 32 * q + lane;
+      const int n0 = nt * BN + 64 * h;
       const int nb = min(n0 / kBlk, p.NB - 1);  // columns past N are not stored
       const float* sw = p.sw + (long long)nb * p.KB;
-      const float* sx = p.sx + m;  // m < ld
-      float acc[HALF];
+      const bool row = m < p.ld;  // the second CTA's rows can lie past the scales' last column
+      const float* sx = p.sx + m;
+      uint64_t acc[32];  // pairs of columns; the sums start from the bias
 #pragma unroll
-      for (int i = 0; i < HALF; ++i) acc[i] = 0.f;
+      for (int i = 0; i < 16; ++i) {
+        const int n = n0 + 4 * i;
+        float4 b4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (n < p.N && SVDQ_INB(p.status, 4ll * n, 16, 4ll * p.N)) b4 = __ldg((const float4*)(p.bias + n));
+        acc[2 * i] = pack2(b4.x, b4.y);
+        acc[2 * i + 1] = pack2(b4.z, b4.w);
+      }
+      // The scales of two blocks ahead: a load is used two folds after it is issued.
       [[maybe_unused]] const long long sx_extent = 4ll * p.KB * p.ld, sw_extent = 4ll * p.NB * p.KB;  // debug build
-      float s_next = 0.f;
-      if (SVDQ_INB(p.status, 4ll * m, 4, sx_extent) && SVDQ_INB(p.status, 4ll * nb * p.KB, 4, sw_extent))
-        s_next = sx[0] * __ldg(sw);
-      for (int j = 0; j < p.KB; ++j, ++it) {
-        const int b = it % T::kBufs;
-        const float s = s_next;
-        if (j + 1 < p.KB && SVDQ_INB(p.status, 4 * ((j + 1) * p.ld + m), 4, sx_extent) &&
-            SVDQ_INB(p.status, 4 * ((long long)nb * p.KB + j + 1), 4, sw_extent))
-          s_next = sx[(j + 1) * p.ld] * __ldg(sw + j + 1);
-        ok = warp_wait(&acc_full[b], (it / T::kBufs) & 1, wc);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * BN + h * HALF);
+      float xs[2], ws[2];
+      auto fetch = [&](int j, int u) {
+        xs[u] = ws[u] = 0.f;
+        if (row && j < p.KB && SVDQ_INB(p.status, 4 * (j * p.ld + m), 4, sx_extent) &&
+            SVDQ_INB(p.status, 4 * ((long long)nb * p.KB + j), 4, sw_extent)) {
+          xs[u] = sx[j * p.ld];
+          ws[u] = __ldg(sw + j);
+        }
+      };
 #pragma unroll
-        for (int c = 0; c < HALF / 32; ++c) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(taddr + 32 * c, r);
-          tmem_ld_wait_regs(r);
-          if (c == HALF / 32 - 1) {  // every column of this accumulator is in registers
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[b]);
+      for (int u = 0; u < 2; ++u) fetch(u, u);
+      for (int j0 = 0; j0 < p.KB && ok; j0 += 2) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (j0 + u >= p.KB) break;
+          const int b = it % T::kBufs;
+          ok = warp_timed_wait(&acc_full[b], (it / T::kBufs) & 1, wc);
+          if (!ok) break;
+          ++it;
+          tc_fence_after();
+          const float s = xs[u] * ws[u];
+          const uint64_t s2 = pack2(s, s);
+          fetch(j0 + u + 2, u);
+          const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * BN + 64 * h);
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(taddr + c, r);
+            tmem_ld_wait_regs(r);
+            if (c == 32) {  // every column of this accumulator is in registers
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                if (PAIR)
+                  mbar_arrive_cluster(dsmem_addr(smem_u32(&acc_empty[b]), 0));
+                else
+                  mbar_arrive(&acc_empty[b]);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[c / 2 + i] = fma2(pack2(r[2 * i], r[2 * i + 1]), s2, acc[c / 2 + i]);
           }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(__uint_as_float(r[i]), s, acc[32 * c + i]);
         }
       }
       if (!ok) break;
       if (m < p.M) {
+        const bool wide = (p.N & 15) == 0 && ((uintptr_t)p.Y & 31) == 0;  // rows of whole 32-byte sectors
 #pragma unroll
-        for (int v = 0; v < HALF / 8; ++v) {  // 8 columns per 16-byte store
-          const int n = n0 + 8 * v;
+        for (int v = 0; v < 4; ++v) {
+          const int n = n0 + 16 * v;
           if (n >= p.N) break;
-          if (!SVDQ_INB(p.status, 2 * ((long long)m * p.N + n), 16, 2ll * p.M * p.N)) break;
-          const float4 b0 = __ldg((const float4*)(p.bias + n)), b1 = __ldg((const float4*)(p.bias + n) + 1);
-          const float bb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-          uint32_t o[4];
+          uint32_t o[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            __nv_bfloat162 hv =
-                __floats2bfloat162_rn(acc[8 * v + 2 * e] + bb[2 * e], acc[8 * v + 2 * e + 1] + bb[2 * e + 1]);
-            o[e] = *(uint32_t*)&hv;
+            const float2 y0 = unpack2(acc[8 * v + 2 * e]), y1 = unpack2(acc[8 * v + 2 * e + 1]);
+            __nv_bfloat162 h0 = __floats2bfloat162_rn(y0.x, y0.y), h1 = __floats2bfloat162_rn(y1.x, y1.y);
+            o[2 * e] = *(uint32_t*)&h0;
+            o[2 * e + 1] = *(uint32_t*)&h1;
           }
-          *(uint4*)(p.Y + (size_t)m * p.N + n) = make_uint4(o[0], o[1], o[2], o[3]);
+          const long long at = (long long)m * p.N + n;
+          if (wide) {
+            if (SVDQ_INB(p.status, 2 * at, 32, 2ll * p.M * p.N)) st_global_32b(p.Y + at, o);
+          } else {
+            if (SVDQ_INB(p.status, 2 * at, 16, 2ll * p.M * p.N))
+              *(uint4*)(p.Y + at) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (n + 8 < p.N && SVDQ_INB(p.status, 2 * at + 16, 16, 2ll * p.M * p.N))
+              *(uint4*)(p.Y + at + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+          }
         }
       }
     }
@@ -305,9 +388,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if constexpr (PAIR) cluster_sync();  // neither CTA is needed by the other's products, loads or barriers any more
+  if (warp == T::kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, T::kCols);
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem, T::kCols);
+    else
+      tmem_dealloc(tmem, T::kCols);
   }
 }
 
@@ -323,27 +410,40 @@ int launch_f8_quantize(const svdq_fp8_layer* L, const void* X, int64_t M, uint8_
              : SVDQ_ERR_CUDA;
 }
 
-template <int BN>
+template <int BN, bool PAIR>
 int launch_f8_tile(const svdq_fp8_layer* L, const F8Maps& maps, F8Params& p, cudaStream_t stream) {
+  using T = Tile<BN, PAIR>;
   {  // the shared-memory attribute belongs to the kernel on each device: set it once per device
     static std::mutex mu;
     static bool attr_set[64] = {};
     if (L->device < 0 || L->device >= 64) return SVDQ_ERR_CUDA;
     std::lock_guard<std::mutex> lock(mu);
     if (!attr_set[L->device]) {
-      if (cudaFuncSetAttribute(k_gemm_fp8<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tile<BN>::kSmem) !=
+      if (cudaFuncSetAttribute(k_gemm_fp8<BN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)T::kSmem) !=
           cudaSuccess)
         return SVDQ_ERR_CUDA;
       attr_set[L->device] = true;
     }
   }
-  p.num_tiles = p.m_tiles * (int)((p.N + BN - 1) / BN);
-  const int sms = device_sm_count(L->device);
-  const int grid = p.num_tiles < sms ? p.num_tiles : sms;
-  return launch_pdl(k_gemm_fp8<BN>, dim3((unsigned)grid), dim3(kGemmThreads), Tile<BN>::kSmem, stream, maps, p) ==
-                 cudaSuccess
-             ? SVDQ_OK
-             : SVDQ_ERR_CUDA;
+  p.m_tiles = (p.M + T::kTileM - 1) / T::kTileM;
+  p.num_tiles = p.m_tiles * ((p.N + BN - 1) / BN);
+  const int slots = device_sm_count(L->device) / (PAIR ? 2 : 1);
+  const int grid = (p.num_tiles < slots ? p.num_tiles : slots) * (PAIR ? 2 : 1);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(T::kThreads);
+  cfg.dynamicSmemBytes = T::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_gemm_fp8<BN, PAIR>, maps, p) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
 }
 
 int launch_f8_gemm(const svdq_fp8_layer* L, int64_t M, void* Y, uint8_t* ws, cudaStream_t stream) {
@@ -358,7 +458,6 @@ int launch_f8_gemm(const svdq_fp8_layer* L, int64_t M, void* Y, uint8_t* ws, cud
   p.N = (int)L->N;
   p.KB = (int)((L->K + kBlk - 1) / kBlk);
   p.NB = (int)((L->N + kBlk - 1) / kBlk);
-  p.m_tiles = (int)((M + 127) / 128);
   p.sx = (const float*)(ws + w.scales);
   p.ld = w.ld;
   p.sw = L->wscales;
@@ -366,23 +465,19 @@ int launch_f8_gemm(const svdq_fp8_layer* L, int64_t M, void* Y, uint8_t* ws, cud
   p.Y = (uint16_t*)Y;
   p.status = (int*)(ws + w.status);
   p.limit = wait_limit_cycles();
-  // Rounds of tiles over the SMs times a tile's cost (its columns, with a fixed part of about 64 for the
-  // rows of X that every tile reads): the narrow tiles fill the SMs when there are few rows.
+  // Rounds of tiles over the SMs times the time of a tile's block: pairs on 256 x 192 where they fill the SMs,
+  // narrower tiles of one CTA where there are too few (a tile's fixed part counts as about 64 columns).
   const int64_t sms = device_sm_count(L->device);
-  int best = 0;
-  int64_t best_cost = 0;
-  const int widths[3] = {256, 128, 64};
-  for (int i = 0; i < 3; ++i) {
-    const int64_t tiles = (int64_t)p.m_tiles * ((L->N + widths[i] - 1) / widths[i]);
-    const int64_t cost = (tiles + sms - 1) / sms * (widths[i] + 64);
-    if (i == 0 || cost < best_cost) {
-      best = i;
-      best_cost = cost;
-    }
-  }
+  auto rounds = [&](int64_t tm, int64_t tn, int64_t slots) {
+    return ((M + tm - 1) / tm * ((L->N + tn - 1) / tn) + slots - 1) / slots;
+  };
+  const int64_t cost[3] = {rounds(256, 192, sms / 2) * (192 + 64), rounds(128, 128, sms) * (128 + 64),
+                           rounds(128, 64, sms) * (64 + 64)};
+  const int best = cost[0] <= cost[1] && cost[0] <= cost[2] ? 0 : (cost[1] <= cost[2] ? 1 : 2);
   maps.b = L->map_w[best];
-  return best == 0 ? launch_f8_tile<256>(L, maps, p, stream)
-                   : best == 1 ? launch_f8_tile<128>(L, maps, p, stream) : launch_f8_tile<64>(L, maps, p, stream);
+  return best == 0 ? launch_f8_tile<192, true>(L, maps, p, stream)
+                   : best == 1 ? launch_f8_tile<128, false>(L, maps, p, stream)
+                               : launch_f8_tile<64, false>(L, maps, p, stream);
 }
 
 }  // namespace
@@ -469,7 +564,7 @@ svdq_status svdq_fp8_layer_create(const void* dev_blob, size_t blob_bytes, int64
   L->bias = (const float*)(base + b.bias);
   L->wscales = (const float*)(base + b.wscales);
   L->wcodes = base + b.wcodes;
-  const uint32_t rows[3] = {256, 128, 64};
+  const uint32_t rows[3] = {96, 128, 64};
   for (int i = 0; i < 3; ++i) {
     if (encode_tmap_2d(&L->map_w[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, L->wcodes, (uint64_t)K, (uint64_t)N, (uint64_t)K,
                        kBlk, rows[i], CU_TENSOR_MAP_SWIZZLE_128B) != SVDQ_OK) {
