@@ -45,7 +45,8 @@ struct Geo {  // DC: 64-wide chunks of the head dimension
   static constexpr int kSlots = DC == 2 ? 4 : 8;
   static constexpr int kTile = DC * kChunkBytes;
   static constexpr int kPartLd = 64 * DC + 4;
-  static constexpr size_t kSmem = 1024 + (size_t)(2 + kSlots) * kTile + 4 * 128 * 4 + 512;
+  static constexpr int kStage = 8 * 32 * 128;  // PAIR: 64 columns of 32 rows a softmax warp; !PAIR: m and l
+  static constexpr size_t kSmem = 1024 + (size_t)(2 + kSlots) * kTile + kStage + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(128 * kPartLd * 4 <= kSlots * kTile, "partial results fit the key/value ring");
 };
@@ -57,6 +58,7 @@ struct AttnParams {
   int row_tiles;   // work items per (sample, item head): tiles (or pairs of tiles) of tokens
   int heads_it;    // item heads: hq / group
   int items;
+  int step, step_rt, step_h, step_b;  // CTAs (clusters) between a CTA's items, and the same divided as an item is
   int ksteps;      // ceil(d / 16)
   int npv;         // d rounded up to 16
   int splits;
@@ -65,6 +67,7 @@ struct AttnParams {
   const int* kv_len;
   const uint8_t* kv_mask;
   long long mask_ld, mask_extent;
+  int o_tma;  // a warp's 32 rows are whole tokens: written by bulk tensor stores
   uint16_t* out;
   long long o_sb, o_st, o_sh, out_extent;  // elements; extent in bytes
   int batch;
@@ -72,7 +75,7 @@ struct AttnParams {
   unsigned long long limit;
 };
 struct AttnMaps {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;  // o (PAIR, o_tma): 64 columns of the 32 rows of a softmax warp
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -81,11 +84,117 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ int keys_of(const AttnParams& p, int b) {
-  if (!p.kv_len) return p.sk;
-  if (!SVDQ_INB(p.status, 4ll * b, 4, 4ll * p.batch)) return 0;
-  const int n = p.kv_len[b];
-  return n < 0 ? 0 : (n > p.sk ? p.sk : n);
+// 2^x of two x <= 126 without the special-function unit, which at 16 results a clock bounds the softmax:
+// x = n + f, n the nearest integer (found by adding 1.5 * 2^23), 2^f by the polynomial of degree 4 with the least
+// relative error on [-1/2, 1/2] (2.7e-6 in binary32, from a Remez exchange), n added to the exponent.
+__device__ __forceinline__ float2 ex2_poly(float2 x) {
+  // smaller ones would need subnormals; 2^-125 adds nothing to a sum that holds 2^-8 or more
+  const uint64_t v = pack2(fmaxf(x.x, -125.f), fmaxf(x.y, -125.f));
+  const uint64_t magic = pack2(12582912.f, 12582912.f), unmagic = pack2(-12582912.f, -12582912.f);
+  const uint64_t t = add2(v, magic);
+  const uint64_t f = fma2(add2(t, unmagic), pack2(-1.f, -1.f), v);
+  uint64_t y = fma2(pack2(0.009570102207362652f, 0.009570102207362652f), f,
+                    pack2(0.05591785907745361f, 0.05591785907745361f));
+  y = fma2(y, f, pack2(0.240247443318367f, 0.240247443318367f));
+  y = fma2(y, f, pack2(0.6931217908859253f, 0.6931217908859253f));
+  y = fma2(y, f, pack2(0.9999992847442627f, 0.9999992847442627f));
+  const float2 yy = unpack2(y), tt = unpack2(t);
+  return make_float2(__uint_as_float(__float_as_uint(yy.x) + (__float_as_uint(tt.x) << 23)),
+                     __uint_as_float(__float_as_uint(yy.y) + (__float_as_uint(tt.y) << 23)));
+}
+// Largest of three; NaN if one is NaN.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// One tile of one row (a thread each): the row of scores at tensor-memory address t_s becomes P there, m and l and, where
+// the maximum has risen, the row of O at t_o follow.  masked: keys whose bit in w is 0 do not count.  Arrives on
+// `part` when three quarters of P are written (its product starts while the last quarter is computed).
+// The scores are read twice, for the maximum and for the exponentials: a row of 128 in registers leaves too few of
+// the 168 a thread has for the rest, and what then goes through local memory costs more than the second read.
+__device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, bool masked, const uint32_t (&w)[4], float c,
+                                             int npv, bool first, float& m, float& l, uint64_t* part, int lane) {
+  float m4[4] = {m, m, m, m};  // four chains
+  if (masked) {  // -inf replaces the scores that do not count, here and for the second read
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t r[32];
+      tmem_ld_32(t_s + 32 * k, r);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) r[j] = (w[k] >> j) & 1u ? r[j] : 0xFF800000u;
+      tmem_st_32x32b_x32(t_s + 32 * k, r);
+#pragma unroll
+      for (int j = 0; j < 32; j += 2)
+        m4[(j >> 1) & 3] = max3(m4[(j >> 1) & 3], __uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+    }
+    tmem_st_wait();
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t r0[32], r1[32];
+      tmem_ld_32x32b_x32(t_s + 64 * h, r0);
+      tmem_ld_32x32b_x32(t_s + 64 * h + 32, r1);
+      tmem_ld_wait_regs(r0);
+      reg_order(r1);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) m4[j & 3] = max3(m4[j & 3], __uint_as_float(r0[j]), __uint_as_float(r1[j]));
+    }
+  }
+  const float mx = max3(m4[0], m4[1], max3(m4[2], m4[3], m4[3]));
+  uint32_t sr[2][32];
+  tmem_ld_32x32b_x32(t_s, sr[0]);
+  if (first) {
+    m = mx;
+  } else if (__any_sync(0xffffffffu, !((mx - m) * c <= kLazy))) {  // risen, or NaN
+    const float f = mx == -INFINITY ? 1.f : ex2((m - mx) * c);
+    m = mx;
+    l *= f;
+    // every product of the previous tile is complete: S of this tile was issued after it
+    for (int cc = 0; cc < npv; cc += 16) {
+      uint32_t o[16];
+      tmem_ld_32x32b_x16(t_o + cc, o);
+      tmem_ld_wait_regs(o);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+      tmem_st_32x32b_x16(t_o + cc, o);
+    }
+  }
+  // m - m: an infinite or NaN maximum makes the whole row NaN, as the formula does
+  const float mc = m == -INFINITY ? 0.f : fmaf(m, c, m - m);
+  const uint64_t c2 = pack2(c, c), nmc2 = pack2(-mc, -mc);
+  uint64_t l2[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t(&r)[32] = sr[k & 1];
+    tmem_ld_wait_regs(r);
+    if (k < 3) tmem_ld_32x32b_x32(t_s + 32 * (k + 1), sr[(k + 1) & 1]);  // ahead of this quarter's exponentials
+    uint32_t pr[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float2 x = unpack2(fma2(pack2(r[2 * j], r[2 * j + 1]), c2, nmc2));
+      const float2 e = (j & 3) == 3 ? ex2_poly(x) : make_float2(ex2(x.x), ex2(x.y));
+      l2[j & 3] = add2(l2[j & 3], pack2(e.x, e.y));
+      __nv_bfloat162 hv = __floats2bfloat162_rn(e.x, e.y);
+      pr[j] = *(uint32_t*)&hv;
+    }
+    tmem_st_32x32b_x16(t_s + 16 * k, pr);  // over scores that are in registers by now
+    if (k == 2) {
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(part);
+    }
+  }
+  const float2 ls = unpack2(add2(add2(l2[0], l2[1]), add2(l2[2], l2[3])));
+  l += ls.x + ls.y;
+  tmem_st_wait();
+}
+
+__device__ __forceinline__ int raw_len(const AttnParams& p, int b) {
+  if (!p.kv_len || !SVDQ_INB(p.status, 4ll * b, 4, 4ll * p.batch)) return p.sk;
+  return __ldg(p.kv_len + b);
 }
 
 // Bits of the 128 keys of tile t that count (the same in every lane).
@@ -102,39 +211,54 @@ __device__ __forceinline__ void key_words(const AttnParams& p, int b, int t, int
   }
 }
 
-// 16 outputs of a row from column `col` on (those below dim), at element `at`; wide: whole 32-byte sectors.
-__device__ __forceinline__ void store_16(const AttnParams& p, long long at, int col, bool wide, const uint32_t (&y)[8]) {
-  if (wide) {
-    if (col < p.d && SVDQ_INB(p.status, 2 * at, 32, p.out_extent)) st_global_32b(p.out + at, y);
-  } else {
-    if (col < p.d && SVDQ_INB(p.status, 2 * at, 16, p.out_extent))
-      *(uint4*)(p.out + at) = make_uint4(y[0], y[1], y[2], y[3]);
-    if (col + 8 < p.d && SVDQ_INB(p.status, 2 * at + 16, 16, p.out_extent))
-      *(uint4*)(p.out + at + 8) = make_uint4(y[4], y[5], y[6], y[7]);
-  }
-}
-
 // One work item: sample, item head, first token of stream 0, key tiles.
 struct Item {
   int b, h, tok0, nkeys, t0, t1;
   bool second;  // PAIR: the second query tile has rows
 };
-template <bool PAIR>
-__device__ __forceinline__ Item item_of(const AttnParams& p, int item, int split) {
-  Item it;
-  const int rt = item % p.row_tiles;
-  const int bh = item / p.row_tiles;
-  it.h = bh % p.heads_it;
-  it.b = bh / p.heads_it;
-  it.tok0 = rt * p.tok_tile * (PAIR ? 2 : 1);
-  it.nkeys = keys_of(p, it.b);
-  const int n = (it.nkeys + kKeys - 1) / kKeys;
-  const int per = (n + p.splits - 1) / p.splits;
-  it.t0 = min(split * per, n);
-  it.t1 = min(it.t0 + per, n);
-  it.second = PAIR && it.tok0 + p.tok_tile < p.sq;
-  return it;
-}
+// Walks a CTA's items without divisions (the step comes divided from the host), and with the length of the next item's
+// sample already asked for: both would otherwise stand between two items' work.
+struct Walk {
+  int item, b, h, rt, len;
+  __device__ __forceinline__ Walk(const AttnParams& p, int first) : item(first) {
+    rt = first % p.row_tiles;
+    const int bh = first / p.row_tiles;
+    h = bh % p.heads_it;
+    b = bh / p.heads_it;
+    len = item < p.items ? raw_len(p, b) : 0;
+  }
+  __device__ __forceinline__ bool more(const AttnParams& p) const { return item < p.items; }
+  template <bool PAIR>
+  __device__ __forceinline__ Item get(const AttnParams& p, int split) const {
+    Item it;
+    it.b = b;
+    it.h = h;
+    it.tok0 = rt * p.tok_tile * (PAIR ? 2 : 1);
+    it.nkeys = max(0, min(len, p.sk));
+    const int n = (it.nkeys + kKeys - 1) / kKeys;
+    if (PAIR) {
+      it.t0 = 0;
+      it.t1 = n;
+    } else {
+      const int per = (n + p.splits - 1) / p.splits;
+      it.t0 = min(split * per, n);
+      it.t1 = min(it.t0 + per, n);
+    }
+    it.second = PAIR && it.tok0 + p.tok_tile < p.sq;
+    return it;
+  }
+  __device__ __forceinline__ void step(const AttnParams& p) {
+    item += p.step;
+    rt += p.step_rt;
+    int c = rt >= p.row_tiles;
+    rt -= c ? p.row_tiles : 0;
+    h += p.step_h + c;
+    c = h >= p.heads_it;
+    h -= c ? p.heads_it : 0;
+    b += p.step_b + c;
+    if (item < p.items) len = raw_len(p, b);
+  }
+};
 
 // Ring position (relative to the item's first) of stream s's tile in iteration i.
 template <bool PAIR>
@@ -153,16 +277,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sm_q = smem;                   // [2][tile]
   uint8_t* sm_kv = smem + 2 * G::kTile;   // [SLOTS][tile]
-  float* sm_m = (float*)(sm_kv + SLOTS * G::kTile);  // [2][128]
+  uint8_t* sm_stage = sm_kv + SLOTS * G::kTile;      // [8][4 KiB]
+  float* sm_m = (float*)sm_stage;                    // [2][128]
   float* sm_l = sm_m + 256;                          // [2][128]
-  uint64_t* q_full = (uint64_t*)(sm_l + 256);        // [2]
+  uint64_t* q_full = (uint64_t*)(sm_stage + G::kStage);  // [2]
   uint64_t* q_empty = q_full + 2;                    // [2]
   uint64_t* kv_full = q_empty + 2;                   // [SLOTS]
   uint64_t* kv_empty = kv_full + SLOTS;              // [SLOTS]
   uint64_t* v_fixed = kv_empty + SLOTS;              // [SLOTS]
   uint64_t* s_full = v_fixed + SLOTS;                // [2]
   uint64_t* p_full = s_full + 2;                     // [2]
-  uint64_t* o_full = p_full + 2;                     // [2]
+  uint64_t* p_part = p_full + 2;                     // [2] three quarters of P are there
+  uint64_t* o_full = p_part + 2;                     // [2]
   uint64_t* mma_done = o_full + 2;
   uint32_t* tmem_slot = (uint32_t*)(mma_done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
@@ -175,6 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
       mbar_init(&q_empty[s], 1);
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 4);  // one arrival per softmax warp of the stream
+      mbar_init(&p_part[s], 4);
       mbar_init(&o_full[s], 1);
     }
     for (int s = 0; s < SLOTS; ++s) {
@@ -200,7 +327,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
   const bool fixing = p.kv_len != nullptr || p.kv_mask != nullptr;
   const int split = PAIR ? 0 : (p.splits > 1 ? (int)cluster_ctarank() : 0);
   const int item0 = PAIR ? (int)blockIdx.x : (int)blockIdx.x / p.splits;
-  const int item_step = PAIR ? (int)gridDim.x : p.items;  // !PAIR: one item per cluster
 
   if (warp == 8) {
     // ------------------------------------------------------------ loads
@@ -222,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         return true;
       };
       const uint32_t q_bytes = (uint32_t)(DC * 128 * p.group * p.tok_tile);
-      for (int item = item0; item < p.items && ok; item += item_step) {
-        const Item it = item_of<PAIR>(p, item, split);
+      for (Walk walk(p, item0); walk.more(p) && ok; walk.step(p)) {
+        const Item it = walk.get<PAIR>(p, split);
         const int n = it.t1 - it.t0;
         if (n == 0) continue;
         const int kvh = (int)((long long)it.h * p.group * p.hk / p.hq);
@@ -286,15 +412,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         }
         umma_commit(&s_full[s]);
       };
-      auto issue_o = [&](int s, int pos, bool first) {
+      auto issue_o = [&](int s, int pos, int k0, int k1, bool first) {
         const uint64_t vd = v_desc + (uint32_t)((pos % SLOTS) * (G::kTile >> 4));
         const uint32_t d = tmem + 256 + s * 128, pa = tmem + s * 128;
-        mma_bf16_ts(d, pa, vd, idesc_o, first ? 0u : 1u);
 #pragma unroll
-        for (int kk = 1; kk < kKeys / 16; ++kk) mma_bf16_ts(d, pa + 8 * kk, vd + 128 * kk, idesc_o, 1u);
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          if (kk >= k0 && kk < k1) mma_bf16_ts(d, pa + 8 * kk, vd + 128 * kk, idesc_o, first && kk == 0 ? 0u : 1u);
       };
-      for (int item = item0; item < p.items && ok; item += item_step) {
-        const Item it = item_of<PAIR>(p, item, split);
+      for (Walk walk(p, item0); walk.more(p) && ok; walk.step(p)) {
+        const Item it = walk.get<PAIR>(p, split);
         const int n = it.t1 - it.t0;
         if (n == 0) continue;
         const int iters = PAIR ? n : (n + 1) / 2;
@@ -316,32 +442,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
           for (int s = 0; s < 2 && ok; ++s) {
             if (!has(i, s)) continue;
             const int vp = base + ring_pos<PAIR>(i, s, true, n);
+            const int kp = base + ring_pos<PAIR>(i + 1, s, false, n);
             const bool last_user = !PAIR || s == 1 || !it.second;
             if (!PAIR || s == 0) {
-              ok = slot_wait(vp);
+              ok = slot_wait(vp) && (!has(i + 1, s) || slot_wait(kp));
               if (ok && fixing) {
                 ok = timed_wait(&v_fixed[fixes % SLOTS], (fixes / SLOTS) & 1, wc);
                 ++fixes;
               }
             }
-            ok = ok && timed_wait(&p_full[s], np[s] & 1, wc);
+            ok = ok && timed_wait(&p_part[s], np[s] & 1, wc);
+            if (!ok) break;
+            tc_fence_after();
+            issue_o(s, vp, 0, 6, i == 0);
+            ok = timed_wait(&p_full[s], np[s] & 1, wc);
             if (!ok) break;
             ++np[s];
             tc_fence_after();
-            issue_o(s, vp, i == 0);
-            if (last_user) umma_commit(&kv_empty[vp % SLOTS]);
+            issue_o(s, vp, 6, 8, false);
             if (has(i + 1, s)) {
-              const int kp = base + ring_pos<PAIR>(i + 1, s, false, n);
-              if (!PAIR || s == 0) {
-                ok = slot_wait(kp);
-                if (!ok) break;
-              }
               issue_s(s, kp);
               if (last_user) umma_commit(&kv_empty[kp % SLOTS]);
               if (PAIR && i + 2 == n) umma_commit(&q_empty[s]);
             } else {
               umma_commit(&o_full[s]);
             }
+            if (last_user) umma_commit(&kv_empty[vp % SLOTS]);
           }
         }
         base += 2 * n;
@@ -355,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
     // of the ring nor falls behind it; rows past the last key of all are zeros already (the loads fill them).
     int base = 0, fixes = 0;
     bool ok = true;
-    for (int item = item0; item < p.items && ok && fixing; item += item_step) {
-      const Item it = item_of<PAIR>(p, item, split);
+    for (Walk walk(p, item0); walk.more(p) && ok && fixing; walk.step(p)) {
+      const Item it = walk.get<PAIR>(p, split);
       const int n = it.t1 - it.t0;
       for (int j = 0; j < n && ok; ++j) {
         const int t = it.t0 + j;
@@ -365,21 +491,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         const int pos = base + (PAIR ? ring_pos<PAIR>(j, 0, true, n) : ring_pos<PAIR>(j >> 1, j & 1, true, n));
         ok = warp_timed_wait(&kv_full[pos % SLOTS], (pos / SLOTS) & 1, wc);
         if (!ok) break;
-        uint8_t* tile = sm_kv + (pos % SLOTS) * G::kTile;
+        uint8_t* tile = sm_kv + (pos % SLOTS) * G::kTile + lane * 16;
+        if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t off = ~w[i];
-          while (off) {  // four rows at a time, eight lanes to a row's 128 bytes
-            uint32_t o2 = off;
-            for (int k = 0; k < (lane >> 3); ++k) o2 &= o2 - 1;
-            if (o2) {
-              const int row = 32 * i + __ffs(o2) - 1;
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t mine = w[i] >> (lane >> 3);  // four rows at a time, eight lanes to a row's 128 bytes
 #pragma unroll
-              for (int ch = 0; ch < DC; ++ch)
-                *(uint4*)(tile + ch * kChunkBytes + row * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            for (int r = 0; r < 32; r += 4) {
+              if (!((mine >> r) & 1u)) {
+#pragma unroll
+                for (int ch = 0; ch < DC; ++ch)
+                  *(uint4*)(tile + ch * kChunkBytes + (32 * i + r) * 128) = make_uint4(0, 0, 0, 0);
+              }
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) off &= off - 1;
           }
         }
         fence_proxy_async_smem();
@@ -398,8 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
     const int r_tok = row / p.group, r_head = row - r_tok * p.group;
     int ns = 0, no = 0;
     bool ok = true;
-    for (int item = item0; item < p.items && ok; item += item_step) {
-      const Item it = item_of<PAIR>(p, item, split);
+    for (Walk walk(p, item0); walk.more(p) && ok;) {
+      const Item it = walk.get<PAIR>(p, split);
+      walk.step(p);
       const int n = it.t1 - it.t0;
       if (PAIR && st == 1 && !it.second) continue;
       const int tok = it.tok0 + (PAIR ? st * p.tok_tile : 0) + r_tok;
@@ -417,58 +542,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         ++ns;
         tc_fence_after();
         if (warp_valid) {
-          uint32_t sr[4][32];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(t_s + 32 * k, sr[k]);
-          tmem_ld_wait_regs(sr[0]);
-#pragma unroll
-          for (int k = 1; k < 4; ++k) reg_order(sr[k]);
-          if (masked) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-              for (int j = 0; j < 32; ++j) sr[k][j] = (w[k] >> j) & 1u ? sr[k][j] : 0xFF800000u;  // -inf
-          }
-          float m4[4] = {m, m, m, m};  // four chains
-#pragma unroll
-          for (int j = 0; j < 32; j += 2)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              m4[k] = fmaxf(fmaxf(m4[k], __uint_as_float(sr[k][j])), __uint_as_float(sr[k][j + 1]));
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          if (i == 0) {
-            m = mx;
-          } else if (__any_sync(0xffffffffu, (mx - m) * p.c > kLazy)) {
-            const float f = mx == -INFINITY ? 1.f : ex2((m - mx) * p.c);
-            m = mx;
-            l *= f;
-            // every product of the previous tile is complete: S of this tile was issued after it
-            for (int cc = 0; cc < p.npv; cc += 16) {
-              uint32_t o[16];
-              tmem_ld_32x32b_x16(t_o + cc, o);
-              tmem_ld_wait_regs(o);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st_32x32b_x16(t_o + cc, o);
-            }
-          }
-          const float mc = m == -INFINITY ? 0.f : m * p.c;
-          float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            uint32_t pr[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float e0 = ex2(fmaf(__uint_as_float(sr[k + (j >> 4)][2 * (j & 15)]), p.c, -mc));
-              const float e1 = ex2(fmaf(__uint_as_float(sr[k + (j >> 4)][2 * (j & 15) + 1]), p.c, -mc));
-              l4[j & 3] += e0 + e1;
-              __nv_bfloat162 hv = __floats2bfloat162_rn(e0, e1);
-              pr[j] = *(uint32_t*)&hv;
-            }
-            tmem_st_32x32b_x32(t_s + 16 * k, pr);
-          }
-          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-          tmem_st_wait();
+          softmax_tile(t_s, t_o, masked, w, p.c, p.npv, i == 0, m, l, &p_part[st], lane);
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_part[st]);
         }
         tc_fence_before();
         __syncwarp();
@@ -483,29 +561,55 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
           tc_fence_after();
         }
         if (warp_valid) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;  // a row without a key: 0
-          const long long off = (long long)it.b * p.o_sb + (long long)tok * p.o_st +
-                                (long long)(it.h * p.group + r_head) * p.o_sh;
-          const bool wide = ((p.o_sb | p.o_st | p.o_sh) & 15) == 0 && ((uintptr_t)p.out & 31) == 0 && (p.d & 15) == 0;
-          for (int cc = 0; cc < p.npv; cc += 32) {
-            uint32_t o[32];
-            if (n > 0) {
-              tmem_ld_32(t_o + cc, o);
+          const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);  // a row without a key: 0
+          uint8_t* mine = sm_stage + warp * 4096;
+          // A thread has a row, but rows lie far apart in memory: 64 columns of the warp's 32 rows go through shared
+          // memory (16-byte pieces, swizzled by the row) and from there as whole 128-byte lines.
+          const bool empty = __any_sync(0xffffffffu, l == 0.f);
+          for (int cc = 0; cc < p.npv; cc += 64) {
+            if (p.o_tma && lane == 0) bulk_wait_read<0>();  // the store before has read its source
+            __syncwarp();
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              uint32_t o[32];
+              if (n > 0) tmem_ld_32(t_o + cc + 32 * hh, o);
+              if (empty) {  // whatever O holds there
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0u : o[j];
+              }
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                uint32_t y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  __nv_bfloat162 hv = __floats2bfloat162_rn(__uint_as_float(o[8 * v + 2 * j]) * inv,
+                                                            __uint_as_float(o[8 * v + 2 * j + 1]) * inv);
+                  y[j] = *(uint32_t*)&hv;
+                }
+                *(uint4*)(mine + lane * 128 + ((4 * hh + v) ^ (lane & 7)) * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+            }
+            if (p.o_tma) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {  // rows past the last token and columns past dim are clipped
+                tma_store_4d(&maps.o, mine, cc, it.h * p.group, tok, it.b);
+                bulk_commit();
+              }
             } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = 0;
-            }
-            uint32_t y[2][8];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              __nv_bfloat162 hv = l == 0.f ? __floats2bfloat162_rn(0.f, 0.f)
-                                           : __floats2bfloat162_rn(__uint_as_float(o[2 * j]) * inv,
-                                                                   __uint_as_float(o[2 * j + 1]) * inv);
-              y[j >> 3][j & 7] = *(uint32_t*)&hv;
-            }
-            if (valid) {
-#pragma unroll
-              for (int v = 0; v < 2; ++v) store_16(p, off + cc + 16 * v, cc + 16 * v, wide, y[v]);
+              __syncwarp();
+              const long long off = (long long)it.b * p.o_sb + (long long)tok * p.o_st +
+                                    (long long)(it.h * p.group + r_head) * p.o_sh;
+              const uint32_t rows_on = __ballot_sync(0xffffffffu, valid);
+              const int col = cc + 8 * (lane & 7);
+              for (int i = 0; i < 8; ++i) {
+                const int r = 4 * i + (lane >> 3);
+                const long long at = __shfl_sync(0xffffffffu, off, r) + col;
+                const uint4 y = *(const uint4*)(mine + r * 128 + ((lane & 7) ^ (r & 7)) * 16);
+                if (col < p.d && (rows_on >> r) & 1u && SVDQ_INB(p.status, 2 * at, 16, p.out_extent))
+                  *(uint4*)(p.out + at) = y;
+              }
+              __syncwarp();
             }
           }
           tc_fence_before();  // these loads come before the products that the next P lets start
@@ -572,6 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
     }
   }
 
+  if (PAIR && p.o_tma && warp < 8 && lane == 0) bulk_wait<0>();
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
@@ -582,8 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
     // Join of the cluster's CTAs: each takes a share of the tile's outputs and reads every CTA's part.
     const bool good = *abort_flag == 0;
     cluster_sync();
-    if (good && item0 < p.items) {
-      const Item it = item_of<PAIR>(p, item0, split);
+    if (good) {
+      const Item it = Walk(p, item0).get<PAIR>(p, split);
       const int toks = min(p.tok_tile, p.sq - it.tok0);
       const int per_row = p.d / 8;
       const int total = toks * p.group * per_row;
@@ -784,6 +889,10 @@ extern "C" svdq_status svdq_cross_attn(const svdq_attn_args* a, int32_t* status,
     while (p.splits < kMaxSplit && bh * tiles * p.splits * 2 <= sms && p.splits * 4 <= ktiles) p.splits *= 2;
   p.row_tiles = (int)(pair ? pairs : tiles);
   p.items = (int)(bh * p.row_tiles);
+  p.step = pair && p.items > sms ? sms : p.items;  // PAIR: persistent CTAs; else one item to a cluster
+  p.step_rt = p.step % p.row_tiles;
+  p.step_h = p.step / p.row_tiles % p.heads_it;
+  p.step_b = p.step / p.row_tiles / p.heads_it;
 
   AttnMaps maps;
   std::memset(&maps, 0, sizeof(maps));
@@ -791,6 +900,13 @@ extern "C" svdq_status svdq_cross_attn(const svdq_attn_args* a, int32_t* status,
                        (uint32_t)p.tok_tile, &p.q_bm, &p.q_hm);
   const int64_t kt = a->kv_tokens > 0 ? a->kv_tokens : 1;
   int st_k = heads_map(&maps.k, kh, a->batch, kt, a->kv_heads, a->dim, 1, kKeys, &p.k_bm, &p.k_hm);
+  if (pair && 32 % p.group == 0) {
+    int bm = 0, hm = 0;
+    p.o_tma = 1;
+    if (heads_map(&maps.o, a->o, a->batch, a->q_tokens, a->heads, a->dim, (uint32_t)p.group, (uint32_t)(32 / p.group), &bm,
+                  &hm) != SVDQ_OK)
+      return SVDQ_ERR_CUDA;
+  }
   int st_v = heads_map(&maps.v, vh, a->batch, kt, a->kv_heads, a->dim, 1, kKeys, &p.v_bm, &p.v_hm);
   if (st_q != SVDQ_OK || st_k != SVDQ_OK || st_v != SVDQ_OK) return SVDQ_ERR_CUDA;
 
@@ -798,7 +914,7 @@ extern "C" svdq_status svdq_cross_attn(const svdq_attn_args* a, int32_t* status,
   const cudaStream_t s = (cudaStream_t)stream;
   const bool wide = p.d > 64;
   if (pair) {
-    const int grid = p.items < sms ? p.items : sms;
+    const int grid = p.step;
     return (svdq_status)(wide ? launch<true, 2>(maps, p, dev, grid, s) : launch<true, 1>(maps, p, dev, grid, s));
   }
   const int grid = p.items * p.splits;
