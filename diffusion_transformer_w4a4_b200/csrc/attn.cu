@@ -15,9 +15,12 @@
 // of 128 rows run in turn, so that one's products overlap the other's exponentials:
 //   PAIR     many rows: the streams are two query tiles that share the key tiles (each key tile is read
 //            once for 256 rows); persistent, one CTA per SM.
-//   !PAIR    few rows: the streams are the even and odd key tiles of one query tile, joined at the end;
+//   !PAIR    fewer rows: the streams are the even and odd key tiles of one query tile, joined at the end;
 //            and a cluster of up to 8 CTAs splits the keys further and joins through distributed shared
 //            memory, in a fixed order (one launch, no workspace, no atomics).
+//   QUART    (!PAIR) 32 rows at most, as in decoding: the rows lie in all four lane quarters of the tile, and a
+//            quarter's warp takes only its quarter of the keys, so that no warp idles and a tile's exponentials
+//            take a quarter of the time; the other quarters' P is zero there, and the quarters are joined too.
 // Rows of a tile are (token, query head of the group) pairs, so heads that share keys share their tiles.
 //
 // Masked keys: scores become -inf by selection, and the masked rows of V are zeroed in shared memory
@@ -48,7 +51,7 @@ struct Geo {  // DC: 64-wide chunks of the head dimension
   static constexpr int kStage = 8 * 32 * 128;  // PAIR: 64 columns of 32 rows a softmax warp; !PAIR: m and l
   static constexpr size_t kSmem = 1024 + (size_t)(2 + kSlots) * kTile + kStage + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
-  static_assert(128 * kPartLd * 4 <= kSlots * kTile, "partial results fit the key/value ring");
+  static_assert(256 * kPartLd * 4 <= (2 + kSlots) * kTile, "partial results fit the query tiles and the ring");
 };
 
 struct AttnParams {
@@ -268,7 +271,55 @@ __device__ __forceinline__ int ring_pos(int i, int s, bool is_v, int n) {
   return 4 * i + (is_v ? (both ? 2 : 1) : 0) + s;
 }
 
-template <bool PAIR, int DC>
+// softmax_tile for QUART: of the tile's keys only those of this warp's lane quarter.
+__device__ __forceinline__ void softmax_quarter(uint32_t t_s, uint32_t t_o, int quarter, uint32_t w, float c, int npv,
+                                                bool first, float& m, float& l) {
+  uint32_t r[32];
+  tmem_ld_32(t_s + 32 * quarter, r);
+  float m4[4] = {m, m, m, m};
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    r[j] = (w >> j) & 1u ? r[j] : 0xFF800000u;
+    m4[j & 3] = max3(m4[j & 3], m4[j & 3], __uint_as_float(r[j]));
+  }
+  const float mx = max3(m4[0], m4[1], max3(m4[2], m4[3], m4[3]));
+  if (first) {
+    m = mx;
+  } else if (__any_sync(0xffffffffu, !((mx - m) * c <= kLazy))) {  // risen, or NaN
+    const float f = mx == -INFINITY ? 1.f : ex2((m - mx) * c);
+    m = mx;
+    l *= f;
+    for (int cc = 0; cc < npv; cc += 16) {
+      uint32_t o[16];
+      tmem_ld_32x32b_x16(t_o + cc, o);
+      tmem_ld_wait_regs(o);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+      tmem_st_32x32b_x16(t_o + cc, o);
+    }
+  }
+  const float mc = m == -INFINITY ? 0.f : fmaf(m, c, m - m);
+  uint32_t pr[16];
+  float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float e0 = ex2(fmaf(__uint_as_float(r[2 * j]), c, -mc)), e1 = ex2(fmaf(__uint_as_float(r[2 * j + 1]), c, -mc));
+    l4[j & 3] += e0 + e1;
+    __nv_bfloat162 hv = __floats2bfloat162_rn(e0, e1);
+    pr[j] = *(uint32_t*)&hv;
+  }
+  l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t z[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) z[j] = k == quarter ? pr[j] : 0u;
+    tmem_st_32x32b_x16(t_s + 16 * k, z);
+  }
+  tmem_st_wait();
+}
+
+template <bool PAIR, int DC, bool QUART>
 __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ AttnMaps maps,
                                                       const __grid_constant__ AttnParams p) {
   using G = Geo<DC>;
@@ -327,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
   const bool fixing = p.kv_len != nullptr || p.kv_mask != nullptr;
   const int split = PAIR ? 0 : (p.splits > 1 ? (int)cluster_ctarank() : 0);
   const int item0 = PAIR ? (int)blockIdx.x : (int)blockIdx.x / p.splits;
+  const Walk only(p, item0);  // (!PAIR) the CTA's item, for the join
 
   if (warp == 8) {
     // ------------------------------------------------------------ loads
@@ -347,7 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         ++pos;
         return true;
       };
-      const uint32_t q_bytes = (uint32_t)(DC * 128 * p.group * p.tok_tile);
+      constexpr int kCopies = QUART ? 4 : 1;
+      const uint32_t q_bytes = (uint32_t)(kCopies * DC * 128 * p.group * p.tok_tile);
       for (Walk walk(p, item0); walk.more(p) && ok; walk.step(p)) {
         const Item it = walk.get<PAIR>(p, split);
         const int n = it.t1 - it.t0;
@@ -361,8 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
           mbar_arrive_expect_tx(&q_full[s], q_bytes);
 #pragma unroll
           for (int ch = 0; ch < DC; ++ch)
-            tma_load_4d(&maps.q, &q_full[s], sm_q + s * G::kTile + ch * kChunkBytes, 64 * ch,
-                        it.h * p.group * p.q_hm, it.tok0 + s * p.tok_tile, it.b * p.q_bm);
+#pragma unroll
+            for (int cp = 0; cp < kCopies; ++cp)
+              tma_load_4d(&maps.q, &q_full[s], sm_q + s * G::kTile + ch * kChunkBytes + cp * 4096, 64 * ch,
+                          it.h * p.group * p.q_hm, it.tok0 + s * p.tok_tile, it.b * p.q_bm);
           ++nq[s];
         }
         if (PAIR) {
@@ -519,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
     const int row = 32 * quarter + lane;
     const uint32_t lanes = (uint32_t)(32 * quarter) << 16;
     const uint32_t t_s = tmem + lanes + st * 128, t_o = tmem + lanes + 256 + st * 128;
-    const int r_tok = row / p.group, r_head = row - r_tok * p.group;
+    const int r_tok = (QUART ? lane : row) / p.group, r_head = (QUART ? lane : row) - r_tok * p.group;
     int ns = 0, no = 0;
     bool ok = true;
     for (Walk walk(p, item0); walk.more(p) && ok;) {
@@ -542,7 +597,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         ++ns;
         tc_fence_after();
         if (warp_valid) {
-          softmax_tile(t_s, t_o, masked, w, p.c, p.npv, i == 0, m, l, &p_part[st], lane);
+          if constexpr (QUART) {
+            const uint32_t wq = masked ? (quarter & 2 ? (quarter & 1 ? w[3] : w[2]) : (quarter & 1 ? w[1] : w[0])) : ~0u;
+            softmax_quarter(t_s, t_o, quarter, wq, p.c, p.npv, i == 0, m, l);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_part[st]);
+          } else {
+            softmax_tile(t_s, t_o, masked, w, p.c, p.npv, i == 0, m, l, &p_part[st], lane);
+          }
         } else {
           tc_fence_before();
           __syncwarp();
@@ -615,62 +678,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
           tc_fence_before();  // these loads come before the products that the next P lets start
         }
       } else {
-        // Join of the two streams: every thread of both arrives here once, also after an expired wait.
-        sm_m[st * 128 + row] = m;
-        sm_l[st * 128 + row] = l;
+        // Parts to be joined: rows of O, not normalised, with m and l, in the place of the query and key tiles (every
+        // product of both streams is complete).
         for (int s = 0; s < 2 && ok; ++s)
           if (s < n) ok = warp_timed_wait(&o_full[s], 0, wc);
-        ok = named_bar_and(1, 256, ok);
         if (!ok) break;
         tc_fence_after();
-        const float m0 = sm_m[row], m1 = sm_m[128 + row];
-        const float mm = fmaxf(m0, m1);
-        const float f0 = m0 == -INFINITY ? 0.f : ex2((m0 - mm) * p.c);
-        const float f1 = m1 == -INFINITY ? 0.f : ex2((m1 - mm) * p.c);
-        const float ll = sm_l[row] * f0 + sm_l[128 + row] * f1;
-        const float inv = 1.f / ll;
-        float* part = (float*)sm_kv;
-        const long long off = (long long)it.b * p.o_sb + (long long)tok * p.o_st +
-                              (long long)(it.h * p.group + r_head) * p.o_sh;
         if (warp_valid) {
-          for (int cc = 16 * st; cc < p.npv; cc += 32) {
-            uint32_t a[16], b[16];
+          const int pr = QUART ? (st * 4 + quarter) * 32 + lane : st * 128 + row;
+          float* part = (float*)smem + pr * G::kPartLd;
+          if (valid) {
+            sm_m[pr] = m;
+            sm_l[pr] = l;
+          }
+          for (int cc = 0; cc < p.npv; cc += 32) {
+            uint32_t o[32];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) a[j] = b[j] = 0;
-            if (n > 0) tmem_ld_32x32b_x16(tmem + lanes + 256 + cc, a);
-            if (n > 1) tmem_ld_32x32b_x16(tmem + lanes + 384 + cc, b);
-            tmem_ld_wait_regs(a);
-            tmem_ld_wait_regs(b);
-            float o[16];
+            for (int j = 0; j < 32; ++j) o[j] = 0;
+            if (my > 0) tmem_ld_32(t_o + cc, o);
+            if (valid) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = fmaf(__uint_as_float(a[j]), f0, __uint_as_float(b[j]) * f1);
-            if (p.splits > 1) {
-              if (valid) {
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                  *(float4*)(part + row * G::kPartLd + cc + 4 * v) =
-                      make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-              }
-            } else if (valid) {
-#pragma unroll
-              for (int v = 0; v < 2; ++v) {
-                uint32_t y[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  __nv_bfloat162 hv = ll == 0.f ? __floats2bfloat162_rn(0.f, 0.f)
-                                                : __floats2bfloat162_rn(o[8 * v + 2 * j] * inv, o[8 * v + 2 * j + 1] * inv);
-                  y[j] = *(uint32_t*)&hv;
-                }
-                if (cc + 8 * v < p.d && SVDQ_INB(p.status, 2 * (off + cc + 8 * v), 16, p.out_extent))
-                  *(uint4*)(p.out + off + cc + 8 * v) = make_uint4(y[0], y[1], y[2], y[3]);
-              }
+              for (int v = 0; v < 8; ++v)
+                *(uint4*)(part + cc + 4 * v) = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
             }
           }
-        }
-        named_bar_sync(1, 256);  // both streams have read m and l
-        if (st == 0) {
-          sm_m[row] = mm;
-          sm_l[row] = ll;
         }
       }
     }
@@ -683,75 +714,147 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (!PAIR && p.splits > 1) {
-    // Join of the cluster's CTAs: each takes a share of the tile's outputs and reads every CTA's part.
+  if (!PAIR) {
+    // Join of the CTA's parts, four columns of a row to a thread, then of the cluster's CTAs, which share the rows out.
+    constexpr int NP = QUART ? 8 : 2, RP = QUART ? 32 : 128;
     const bool good = *abort_flag == 0;
-    cluster_sync();
+    const int tok0 = only.rt * p.tok_tile;
+    const int per_row = p.d / 4;
+    const int total = min(p.tok_tile, p.sq - tok0) * p.group * per_row;
+    float* part = (float*)smem;
+    float* fm = (float*)(sm_stage + 2048);  // [128] of the CTA
+    float* fl = fm + 128;                   // [128]
+    auto store = [&](int row, int col, const float (&o)[4], float ll) {
+      const float inv = 1.f / ll;
+      uint32_t y[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        __nv_bfloat162 hv = __floats2bfloat162_rn(o[2 * j] * inv, o[2 * j + 1] * inv);
+        y[j] = ll == 0.f ? 0u : *(uint32_t*)&hv;
+      }
+      const int tok = tok0 + row / p.group, head = only.h * p.group + row % p.group;
+      const long long off = (long long)only.b * p.o_sb + (long long)tok * p.o_st + (long long)head * p.o_sh + col;
+      if (SVDQ_INB(p.status, 2 * off, 8, p.out_extent)) *(uint2*)(p.out + off) = make_uint2(y[0], y[1]);
+    };
     if (good) {
-      const Item it = Walk(p, item0).get<PAIR>(p, split);
-      const int toks = min(p.tok_tile, p.sq - it.tok0);
-      const int per_row = p.d / 8;
-      const int total = toks * p.group * per_row;
-      const uint32_t part = smem_u32(sm_kv), pm = smem_u32(sm_m), pl = smem_u32(sm_l);
-      for (int idx = split * kThreads + threadIdx.x; idx < total; idx += p.splits * kThreads) {
-        const int row = idx / per_row, col = (idx - row * per_row) * 8;
-        float mr[kMaxSplit];
-        float mm = -INFINITY;
+      for (int u = threadIdx.x; u < total; u += kThreads) {
+        const int row = u / per_row, col = (u - row * per_row) * 4;
+        float f[NP], mm = -INFINITY, ll = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r) {
-          mr[r] = r < p.splits ? dsmem_ld_f32(dsmem_addr(pm + 4 * row, r)) : -INFINITY;
-          mm = fmaxf(mm, mr[r]);
+        for (int k = 0; k < NP; ++k) {
+          f[k] = sm_m[k * RP + row];
+          mm = fmaxf(mm, f[k]);
         }
-        float ll = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r) {
-          if (r < p.splits) {
-            const float lr = dsmem_ld_f32(dsmem_addr(pl + 4 * row, r));
-            const uint32_t pa = dsmem_addr(part + (uint32_t)(row * G::kPartLd + col) * 4, r);
-            const float4 x = dsmem_ld_f32x4(pa), y = dsmem_ld_f32x4(pa + 16);
-            const float f = mr[r] == -INFINITY ? 0.f : ex2((mr[r] - mm) * p.c);
-            ll = fmaf(lr, f, ll);
-            o[0] = fmaf(x.x, f, o[0]);
-            o[1] = fmaf(x.y, f, o[1]);
-            o[2] = fmaf(x.z, f, o[2]);
-            o[3] = fmaf(x.w, f, o[3]);
-            o[4] = fmaf(y.x, f, o[4]);
-            o[5] = fmaf(y.y, f, o[5]);
-            o[6] = fmaf(y.z, f, o[6]);
-            o[7] = fmaf(y.w, f, o[7]);
+        for (int k = 0; k < NP; ++k) {
+          const float4 x = *(const float4*)(part + (k * RP + row) * G::kPartLd + col);
+          f[k] = f[k] == -INFINITY ? 0.f : ex2((f[k] - mm) * p.c);
+          ll = fmaf(sm_l[k * RP + row], f[k], ll);
+          o[0] = fmaf(x.x, f[k], o[0]);
+          o[1] = fmaf(x.y, f[k], o[1]);
+          o[2] = fmaf(x.z, f[k], o[2]);
+          o[3] = fmaf(x.w, f[k], o[3]);
+        }
+        if (p.splits == 1) {
+          store(row, col, o, ll);
+        } else {  // over the first part, whose place no other thread reads
+          *(float4*)(part + row * G::kPartLd + col) = make_float4(o[0], o[1], o[2], o[3]);
+          if (col == 0) {
+            fm[row] = mm;
+            fl[row] = ll;
           }
         }
-        const float inv = 1.f / ll;
-        uint32_t y[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          __nv_bfloat162 hv = ll == 0.f ? __floats2bfloat162_rn(0.f, 0.f)
-                                        : __floats2bfloat162_rn(o[2 * j] * inv, o[2 * j + 1] * inv);
-          y[j] = *(uint32_t*)&hv;
-        }
-        const int tok = it.tok0 + row / p.group, head = it.h * p.group + row % p.group;
-        const long long off = (long long)it.b * p.o_sb + (long long)tok * p.o_st + (long long)head * p.o_sh + col;
-        if (SVDQ_INB(p.status, 2 * off, 16, p.out_extent)) *(uint4*)(p.out + off) = make_uint4(y[0], y[1], y[2], y[3]);
       }
     }
-    cluster_sync();  // a CTA's shared memory stays until every other has read it
+    if (p.splits > 1) {
+      cluster_sync();
+      if (good) {
+        const uint32_t a_part = smem_u32(part), a_m = smem_u32(fm), a_l = smem_u32(fl);
+        for (int u = threadIdx.x * p.splits + split; u < total; u += kThreads * p.splits) {
+          const int row = u / per_row, col = (u - row * per_row) * 4;
+          float fr[kMaxSplit], lr[kMaxSplit];
+          float4 x[kMaxSplit];
+#pragma unroll
+          for (int r = 0; r < kMaxSplit; ++r) {  // all asked for before the first is used
+            if (r < p.splits) {
+              fr[r] = dsmem_ld_f32(dsmem_addr(a_m + 4 * row, r));
+              lr[r] = dsmem_ld_f32(dsmem_addr(a_l + 4 * row, r));
+              x[r] = dsmem_ld_f32x4(dsmem_addr(a_part + (uint32_t)(row * G::kPartLd + col) * 4, r));
+            } else {
+              fr[r] = -INFINITY;
+              lr[r] = 0.f;
+              x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          }
+          float mm = -INFINITY, ll = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int r = 0; r < kMaxSplit; ++r) mm = fmaxf(mm, fr[r]);
+#pragma unroll
+          for (int r = 0; r < kMaxSplit; ++r) {
+            const float f = fr[r] == -INFINITY ? 0.f : ex2((fr[r] - mm) * p.c);
+            ll = fmaf(lr[r], f, ll);
+            o[0] = fmaf(x[r].x, f, o[0]);
+            o[1] = fmaf(x[r].y, f, o[1]);
+            o[2] = fmaf(x[r].z, f, o[2]);
+            o[3] = fmaf(x[r].w, f, o[3]);
+          }
+          store(row, col, o, ll);
+        }
+      }
+      cluster_sync();  // a CTA's shared memory stays until every other has read it
+    }
   }
 }
 
-template <bool PAIR, int DC>
-int launch(const AttnMaps& maps, const AttnParams& p, int dev, int grid, cudaStream_t stream) {
-  {  // the shared-memory attribute belongs to the kernel on each device: set it once per device
-    static std::mutex mu;
-    static bool attr_set[64] = {};
-    if (dev < 0 || dev >= 64) return SVDQ_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!attr_set[dev]) {
-      if (cudaFuncSetAttribute(k_attn<PAIR, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)Geo<DC>::kSmem) != cudaSuccess)
-        return SVDQ_ERR_CUDA;
-      attr_set[dev] = true;
+// Once per device: the shared-memory attribute (it belongs to the kernel on each device), and how many clusters of each
+// size are resident at once (a cluster lies inside one GPC, so that 148 SMs hold 15 clusters of 8, not 18).
+struct DeviceFit {
+  bool set = false;
+  int clusters[kMaxSplit + 1] = {};
+};
+template <bool PAIR, int DC, bool QUART>
+const DeviceFit* device_fit(int dev) {
+  static std::mutex mu;
+  static DeviceFit fits[64];
+  if (dev < 0 || dev >= 64) return nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  DeviceFit& f = fits[dev];
+  if (!f.set) {
+    const auto kern = k_attn<PAIR, DC, QUART>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo<DC>::kSmem) != cudaSuccess)
+      return nullptr;
+    for (int c = 2; !PAIR && c <= kMaxSplit; ++c) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)(148 * c));
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = Geo<DC>::kSmem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = (unsigned)c;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&f.clusters[c], kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        f.clusters[c] = 0;
+      }
     }
+    f.set = true;
   }
+  return &f;
+}
+
+template <bool PAIR, int DC, bool QUART>
+int launch(const AttnMaps& maps, AttnParams& p, int dev, cudaStream_t stream) {
+  const DeviceFit* fit = device_fit<PAIR, DC, QUART>(dev);
+  if (!fit) return SVDQ_ERR_CUDA;
+  p.splits = 1;
+  // The largest cluster of which one for each item is resident at once, with two key tiles to a CTA.
+  const int ktiles = (p.sk + kKeys - 1) / kKeys;
+  for (int c = 2; !PAIR && c <= kMaxSplit && 2 * c <= ktiles; ++c)
+    if (p.items <= fit->clusters[c]) p.splits = c;
+  const int grid = PAIR ? p.step : p.items * p.splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
@@ -766,7 +869,7 @@ int launch(const AttnMaps& maps, const AttnParams& p, int dev, int grid, cudaStr
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_attn<PAIR, DC>, maps, p) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k_attn<PAIR, DC, QUART>, maps, p) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
 }
 
 // Tensor map of a [batch, tokens, heads, dim] view.  A dimension of size one, or one with
@@ -858,7 +961,9 @@ extern "C" svdq_status svdq_cross_attn(const svdq_attn_args* a, int32_t* status,
   // Query heads of one key head go into the rows of one tile; a broadcast query head, or more
   // of them than a tile has rows, is taken head by head.
   p.group = share <= kRows && (share == 1 || a->q.stride_head != 0) ? share : 1;
-  p.tok_tile = kRows / p.group;
+  // Few rows: one tile, held by each of its lane quarters.
+  const bool quart = p.group <= 32 && (int64_t)p.sq * p.group <= 32;
+  p.tok_tile = (quart ? 32 : kRows) / p.group;
   p.heads_it = p.hq / p.group;
   p.ksteps = (p.d + 15) / 16;
   p.npv = p.ksteps * 16;
@@ -879,14 +984,10 @@ extern "C" svdq_status svdq_cross_attn(const svdq_attn_args* a, int32_t* status,
   const int64_t bh = (int64_t)p.batch * p.heads_it;
   const int64_t tiles = ((int64_t)p.sq + p.tok_tile - 1) / p.tok_tile;
   const int64_t pairs = (tiles + 1) / 2;
-  const int ktiles = (p.sk + kKeys - 1) / kKeys;
-  // Pairs of tiles once they fill the SMs; below that single tiles, whose keys are split over the SMs
-  // that would stay idle, two key tiles to a CTA at least.
-  const bool pair = bh * pairs >= sms;
+  // Pairs of tiles once they fill the SMs; below that single tiles, whose keys are split over the SMs that would
+  // stay idle.
+  const bool pair = !quart && bh * pairs >= sms;
   if (bh * tiles > ((int64_t)1 << 30)) return SVDQ_ERR_INVALID_ARG;
-  p.splits = 1;
-  if (!pair)
-    while (p.splits < kMaxSplit && bh * tiles * p.splits * 2 <= sms && p.splits * 4 <= ktiles) p.splits *= 2;
   p.row_tiles = (int)(pair ? pairs : tiles);
   p.items = (int)(bh * p.row_tiles);
   p.step = pair && p.items > sms ? sms : p.items;  // PAIR: persistent CTAs; else one item to a cluster
@@ -913,10 +1014,9 @@ extern "C" svdq_status svdq_cross_attn(const svdq_attn_args* a, int32_t* status,
   NvtxRange range("svdq/cross_attn");
   const cudaStream_t s = (cudaStream_t)stream;
   const bool wide = p.d > 64;
-  if (pair) {
-    const int grid = p.step;
-    return (svdq_status)(wide ? launch<true, 2>(maps, p, dev, grid, s) : launch<true, 1>(maps, p, dev, grid, s));
-  }
-  const int grid = p.items * p.splits;
-  return (svdq_status)(wide ? launch<false, 2>(maps, p, dev, grid, s) : launch<false, 1>(maps, p, dev, grid, s));
+  if (pair)
+    return (svdq_status)(wide ? launch<true, 2, false>(maps, p, dev, s) : launch<true, 1, false>(maps, p, dev, s));
+  if (quart)
+    return (svdq_status)(wide ? launch<false, 2, true>(maps, p, dev, s) : launch<false, 1, true>(maps, p, dev, s));
+  return (svdq_status)(wide ? launch<false, 2, false>(maps, p, dev, s) : launch<false, 1, false>(maps, p, dev, s));
 }
