@@ -13,7 +13,6 @@ steps between a block's projections, take torch tensors [batch, tokens, heads, d
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import struct
@@ -758,7 +757,9 @@ def svdq_fp8_gemm(h, M: int, Y, ws, stream=None) -> None:
 
 
 def svdq_fp8_forward(h, X, M: int, Y, ws, stream=None) -> None:
-    _check(lib().svdq_fp8_forward(h, _ptr(X), M, _ptr(Y), _ptr(ws), ws.numel(), _stream(stream)), "svdq_fp8_forward")
+    st = lib().svdq_fp8_forward(h, _ptr(X), M, _ptr(Y), ws.data_ptr(), ws.numel(), _stream(stream))
+    if st != SVDQ_OK:
+        raise SvdqError(st, "svdq_fp8_forward")
 
 
 def svdq_fp8_read_status(h, M: int, ws) -> int:
@@ -796,17 +797,22 @@ class Fp8Linear:
         return self._ws[M]
 
     def forward(self, x, out=None, stream=None):
-        torch = _torch()
-        _check_input(x, self.K, self.device)
+        torch, device = _torch(), self.device
+        _check_input(x, self.K, device)
         M = x.numel() // self.K
         if out is None:
-            out = torch.empty(M, self.N, dtype=torch.bfloat16, device=self.device)
-        elif not (out.dtype == torch.bfloat16 and out.device == self.device and out.is_contiguous()
+            out = torch.empty(M, self.N, dtype=torch.bfloat16, device=device)
+        elif not (out.dtype == torch.bfloat16 and out.device == device and out.is_contiguous()
                   and out.numel() == M * self.N):
-            raise ValueError(f"expected a contiguous bf16 output [{M}, {self.N}] on {self.device}")
-        ws = self.workspace(M)
-        with _on(self.device):
-            svdq_fp8_forward(self.handle, x, M, out, ws, _stream_of(stream, self.device))
+            raise ValueError(f"expected a contiguous bf16 output [{M}, {self.N}] on {device}")
+        ws = self._ws.get(M)
+        if ws is None:
+            ws = self.workspace(M)
+        if torch.cuda.current_device() == device.index:
+            svdq_fp8_forward(self.handle, x, M, out, ws, _stream_of(stream, device))
+        else:
+            with torch.cuda.device(device):
+                svdq_fp8_forward(self.handle, x, M, out, ws, _stream_of(stream, device))
         return out
 
     __call__ = forward
@@ -834,13 +840,18 @@ _ROPE_ARGS = struct.Struct("P3qP3q3qPPqP")  # svdq_norm_rope_args
 _ATTN_ARGS = struct.Struct("P3qP3qP3qP3q6qPPqf4x")  # svdq_attn_args
 PAIRS = {"interleaved": 0, "halves": 1}
 _attn_status = {}
-_NO_CONTEXT = contextlib.nullcontext()
 
 
-def _on(device):
-    """A context with `device` current (nothing to do, and nothing spent, where it is already)."""
+def _call_on(device, where, fn, *args):
+    """fn(*args), a library call that returns a status, with `device` current."""
     cuda = _torch().cuda
-    return _NO_CONTEXT if cuda.current_device() == device.index else cuda.device(device)
+    if cuda.current_device() == device.index:
+        st = fn(*args)
+    else:
+        with cuda.device(device):
+            st = fn(*args)
+    if st != SVDQ_OK:
+        raise SvdqError(st, where)
 
 
 def attn_status(device=None):
@@ -905,35 +916,36 @@ def svdq_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, *, eps=1e-6, rope
         raise ValueError("positions need a rope table")
     packed = [None, None]
     outs = [out_q, out_k]
-    for i, (name, x, w) in enumerate((("q", q, q_weight), ("k", k, k_weight))):
-        if x is None:
-            continue
-        xa = _heads(name, x, device)
+    for i in (0, 1) if k is not None else (0,):
+        x, w, out = (k, k_weight, out_k) if i else (q, q_weight, out_q)
+        xa = _heads("qk"[i], x, device)
         shape = x.shape
         b, s, h, d = shape
-        if outs[i] is None:
-            outs[i] = torch.empty_like(x)
-            ya = outs[i].data_ptr(), *outs[i].stride()[:3]
+        if out is None:
+            out = outs[i] = torch.empty_like(x)
+            yb, yt, yh, _ = out.stride()
+            ya = out.data_ptr(), yb, yt, yh
         else:
-            ya = _heads("out_" + name, outs[i], device)
-            if outs[i].shape != shape:
-                raise ValueError(f"out_{name}: {tuple(outs[i].shape)} for {tuple(shape)}")
+            ya = _heads("out_" + "qk"[i], out, device)
+            if out.shape != shape:
+                raise ValueError(f"out_{'qk'[i]}: {tuple(out.shape)} for {tuple(shape)}")
         wp = 0
         if w is not None:
-            _check_aux(name + "_weight", w, torch.bfloat16, (d,), device)
+            _check_aux("weight of " + "qk"[i], w, torch.bfloat16, (d,), device)
             wp = w.data_ptr()
-        if positions is not None:
-            if i == 0:
+        if i == 0:
+            dim = d
+            if positions is not None:
                 _check_aux("positions", positions, torch.int32, (b, s), device)
                 pos = positions.data_ptr()
-            elif positions.shape != (b, s):
+        else:
+            if d != dim:
+                raise ValueError(f"heads of {dim} (q) and {d} (k)")
+            if pos and positions.shape != (b, s):
                 raise ValueError(f"positions {tuple(positions.shape)} for k {tuple(shape)}")
-        if i == 1 and d != q.shape[3]:
-            raise ValueError(f"heads of {q.shape[3]} (q) and {d} (k)")
         packed[i] = _ROPE_ARGS.pack(*xa, *ya, b, s, h, wp, table, rows, pos)
-    with _on(device):
-        _check(lib().svdq_qk_norm_rope(packed[0], packed[1], q.shape[3], rot, PAIRS[pairs], eps,
-                                       _status_ptr(status, device), _stream_of(stream, device)), "svdq_qk_norm_rope")
+    _call_on(device, "svdq_qk_norm_rope", lib().svdq_qk_norm_rope, packed[0], packed[1], dim, rot, PAIRS[pairs],
+             eps, _status_ptr(status, device), _stream_of(stream, device))
     return outs[0] if k is None else (outs[0], outs[1])
 
 
@@ -969,6 +981,6 @@ def svdq_cross_attn(q, k, v, *, kv_len=None, kv_mask=None, scale=None, out=None,
         mask, mask_ld = kv_mask.data_ptr(), kv_mask.stride(0)
     args = _ATTN_ARGS.pack(*qa, *ka, *va, *oa, b, sq, sk, h, hk, d, lens, mask, mask_ld,
                            d ** -0.5 if scale is None else scale)
-    with _on(device):
-        _check(lib().svdq_cross_attn(args, _status_ptr(status, device), _stream_of(stream, device)), "svdq_cross_attn")
+    _call_on(device, "svdq_cross_attn", lib().svdq_cross_attn, args, _status_ptr(status, device),
+             _stream_of(stream, device))
     return out

@@ -45,109 +45,176 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
   }
 }
 
-// UNROLL heads of one token at a time; PAIRS: 0 adjacent, 1 halves.
+// One token of one side.  PAIRS: 0 adjacent, 1 halves.  The weight is multiplied into the cosines and sines once, so
+// that an output costs a product with 1/rms, a product and a fused multiply-add (two outputs to an instruction for
+// adjacent pairs); the kernel issues about as long as it moves data, so instructions count.
+// `u` holds the first heads' elements, asked for before anything else of the token.
+constexpr int kUnroll = 3;  // heads of a lane in flight for each side
+struct Place {
+  int b, s;
+};
+__device__ __forceinline__ Place place_of(const Side& sd, long long token) {
+  const unsigned t = (unsigned)token, n = (unsigned)sd.tokens;  // batch * tokens <= 2^30
+  return {(int)(t / n), (int)(t % n)};
+}
+template <int LG>
+__device__ __forceinline__ void load_heads(const NormParams& p, const Side& sd, const Place& at, int h0,
+                                           uint4 (&u)[kUnroll]) {
+  constexpr int ROWS = kThreads / LG;
+  const int e0 = 8 * (threadIdx.x % LG);
+  const long long xb = at.b * sd.x_sb + at.s * sd.x_st + e0;
+#pragma unroll
+  for (int k = 0; k < kUnroll; ++k) {
+    const int h = h0 + k * ROWS + (int)threadIdx.x / LG;
+    u[k] = make_uint4(0, 0, 0, 0);
+    const long long off = xb + (long long)h * sd.x_sh;
+    if (e0 < p.dim && h < sd.heads && SVDQ_INB(p.status, 2 * off, 16, sd.x_extent)) u[k] = *(const uint4*)(sd.x + off);
+  }
+}
 template <int LG, int PAIRS>
-__device__ __forceinline__ void do_side(const NormParams& p, const Side& sd, long long token) {
-  constexpr int ROWS = kThreads / LG, UNROLL = 4;
+__device__ __forceinline__ void do_side(const NormParams& p, const Side& sd, long long token, const Place& place,
+                                        uint4 (&u)[kUnroll]) {
+  constexpr int ROWS = kThreads / LG, UNROLL = kUnroll;
   const int sub = threadIdx.x % LG, first = threadIdx.x / LG;
   const int e0 = 8 * sub;
   const bool on = e0 < p.dim;
-  const int b = (int)(token / sd.tokens), s = (int)(token - (long long)b * sd.tokens);
-  float w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = 1.f;
-  if (sd.weight && on && SVDQ_INB(p.status, 2 * e0, 16, 2 * p.dim)) unpack(__ldg((const uint4*)(sd.weight + e0)), w);
-  // cosine and sine of this lane's pairs (adjacent: 4; halves: one for each element)
-  constexpr int NP = PAIRS == 0 ? 4 : 8;
-  float cs[NP], sn[NP];
-#pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    cs[i] = 1.f;
-    sn[i] = 0.f;
-  }
+  const int b = place.b, s = place.s;
   const int half = p.rot >> 1;
+  const float* r = nullptr;  // the token's row of cosines and sines
+  [[maybe_unused]] long long row = s;
   bool bad = false;
-  if (sd.rope && p.rot > 0) {
-    long long row = s;
+  if (sd.rope) {
     if (sd.positions) {
       row = SVDQ_INB(p.status, 4 * token, 4, 4ll * sd.batch * sd.tokens) ? (long long)__ldg(sd.positions + token) : -1;
       bad = row < 0 || row >= sd.rope_rows;
       if (bad) row = 0;
     }
-    const float* r = sd.rope + row * p.rot;
+    r = sd.rope + row * p.rot;
+  }
+  if (bad && p.status && threadIdx.x == 0) atomicCAS(p.status, 0, SVDQ_ERR_INVALID_ARG);
+  float w[8];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {  // four elements: two adjacent pairs, or four halves' pairs
-      const int e = e0 + 4 * g;
-      if (e >= p.rot) continue;
-      const int at = PAIRS == 0 ? e : 2 * (e < half ? e : e - half);  // floats from the row's start
-      if (!SVDQ_INB(p.status, 4 * (row * p.rot + at), PAIRS == 0 ? 16 : 32, 4 * sd.rope_rows * p.rot)) continue;
+  for (int i = 0; i < 8; ++i) w[i] = 1.f;
+  if (sd.weight && on && SVDQ_INB(p.status, 2 * e0, 16, 2 * p.dim)) unpack(__ldg((const uint4*)(sd.weight + e0)), w);
+  // Coefficients of a lane's eight elements, four (g) at a time; ca multiplies the element, cb its partner.
+  // Adjacent: packed over the group's two pairs, [g][0] for the first of a pair, [g][1] for the second.
+  uint64_t ca2[2][2], cb2[2][2];
+  float ca[8], cb[8];
+  bool turned[2];
 #pragma unroll
-      for (int v = 0; v < (PAIRS == 0 ? 1 : 2); ++v) {
-        const float4 t = __ldg((const float4*)(r + at) + v);
-        const int i = PAIRS == 0 ? 2 * g : 4 * g + 2 * v;
-        cs[i] = t.x;
-        sn[i] = t.y;
-        cs[i + 1] = t.z;
-        sn[i + 1] = t.w;
+  for (int g = 0; g < 2; ++g) {
+    const int e = e0 + 4 * g;
+    turned[g] = r != nullptr && e < p.rot;
+    if constexpr (PAIRS == 0) {
+      float4 t = make_float4(1.f, 0.f, 1.f, 0.f);
+      if (turned[g] && SVDQ_INB(p.status, 4 * (row * p.rot + e), 16, 4 * sd.rope_rows * p.rot))
+        t = __ldg((const float4*)(r + e));
+      const float* v = w + 4 * g;
+      ca2[g][0] = pack2(v[0] * t.x, v[2] * t.z);
+      cb2[g][0] = pack2(-v[1] * t.y, -v[3] * t.w);
+      ca2[g][1] = pack2(v[1] * t.x, v[3] * t.z);
+      cb2[g][1] = pack2(v[0] * t.y, v[2] * t.w);
+    } else {
+      float pw[4] = {1.f, 1.f, 1.f, 1.f};  // the partners' weights
+      const int at = e < half ? e : e - half;
+      const int pe = e < half ? e + half : e - half;
+      if (turned[g] && sd.weight && SVDQ_INB(p.status, 2 * pe, 8, 2 * p.dim)) {
+        const uint2 u = __ldg((const uint2*)(sd.weight + pe));
+        pw[0] = __uint_as_float(u.x << 16);
+        pw[1] = __uint_as_float(u.x & 0xFFFF0000u);
+        pw[2] = __uint_as_float(u.y << 16);
+        pw[3] = __uint_as_float(u.y & 0xFFFF0000u);
       }
-      if (PAIRS == 1 && e < half) {  // the first of a pair subtracts
+      float4 t0 = make_float4(1.f, 0.f, 1.f, 0.f), t1 = t0;
+      if (turned[g] && SVDQ_INB(p.status, 4 * (row * p.rot + 2 * at), 32, 4 * sd.rope_rows * p.rot)) {
+        t0 = __ldg((const float4*)(r + 2 * at));
+        t1 = __ldg((const float4*)(r + 2 * at) + 1);
+      }
+      const float cs[4] = {t0.x, t0.z, t1.x, t1.z}, sn[4] = {t0.y, t0.w, t1.y, t1.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sn[4 * g + i] = -sn[4 * g + i];
+      for (int i = 0; i < 4; ++i) {
+        ca[4 * g + i] = w[4 * g + i] * cs[i];
+        cb[4 * g + i] = (e < half ? -sn[i] : sn[i]) * pw[i];  // the first of a pair subtracts
       }
     }
   }
-  if (bad && p.status && threadIdx.x == 0) atomicCAS(p.status, 0, SVDQ_ERR_INVALID_ARG);
-  const long long xb = b * sd.x_sb + s * sd.x_st, yb = b * sd.y_sb + s * sd.y_st;
+  const long long yb = b * sd.y_sb + s * sd.y_st;
+  const float inv_dim = 1.f / (float)p.dim;
   // every lane takes every round (the shuffles need whole warps); heads past the last read nothing
   for (int h0 = 0; h0 < sd.heads; h0 += ROWS * UNROLL) {
-    uint4 u[UNROLL];
-#pragma unroll
-    for (int k = 0; k < UNROLL; ++k) {
-      const int h = h0 + k * ROWS + first;
-      u[k] = make_uint4(0, 0, 0, 0);
-      const long long off = xb + (long long)h * sd.x_sh + e0;
-      if (on && h < sd.heads && SVDQ_INB(p.status, 2 * off, 16, sd.x_extent)) u[k] = *(const uint4*)(sd.x + off);
-    }
+    if (h0 > 0) load_heads<LG>(p, sd, place, h0, u);
 #pragma unroll
     for (int k = 0; k < UNROLL; ++k) {
       if (h0 + k * ROWS >= sd.heads) break;
       const int h = h0 + k * ROWS + first;
-      float v[8];
-      unpack(u[k], v);
-      float ss = 0.f;
+      const uint32_t in[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+      // lo[g]: first and third element of the group, hi[g]: second and fourth
+      uint64_t lo[2], hi[2], ss2 = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+      for (int g = 0; g < 2; ++g) {
+        lo[g] = pack2(in[2 * g] << 16, in[2 * g + 1] << 16);
+        hi[g] = pack2(in[2 * g] & 0xFFFF0000u, in[2 * g + 1] & 0xFFFF0000u);
+        ss2 = fma2(lo[g], lo[g], ss2);
+        ss2 = fma2(hi[g], hi[g], ss2);
+      }
+      const float2 sp = unpack2(ss2);
+      float ss = sp.x + sp.y;
 #pragma unroll
       for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      float r = rsqrtf(ss / (float)p.dim + p.eps);
-      if (bad) r = __int_as_float(0x7FC00000);
+      float inv = rsqrtf(fmaf(ss, inv_dim, p.eps));
+      if (bad) inv = __int_as_float(0x7FC00000);
+      const uint64_t inv2 = pack2(inv, inv);
+      float2 y[2][2];  // [g][0] of the firsts of the group's pairs, [g][1] of the seconds
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= r * w[i];
-      float y[8];
-      if (PAIRS == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[2 * i] = v[2 * i] * cs[i] - v[2 * i + 1] * sn[i];
-          y[2 * i + 1] = v[2 * i] * sn[i] + v[2 * i + 1] * cs[i];
+      for (int g = 0; g < 2; ++g) {
+        lo[g] = mul2(lo[g], inv2);
+        hi[g] = mul2(hi[g], inv2);
+        if constexpr (PAIRS == 0) {
+          uint64_t a = mul2(lo[g], ca2[g][0]), c = mul2(hi[g], ca2[g][1]);
+          if (turned[g]) {
+            a = fma2(hi[g], cb2[g][0], a);
+            c = fma2(lo[g], cb2[g][1], c);
+          }
+          y[g][0] = unpack2(a);
+          y[g][1] = unpack2(c);
         }
-      } else {
+      }
+      if constexpr (PAIRS == 1) {
+        float v[8];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const float2 l = unpack2(lo[g]), q = unpack2(hi[g]);
+          v[4 * g] = l.x;
+          v[4 * g + 1] = q.x;
+          v[4 * g + 2] = l.y;
+          v[4 * g + 3] = q.y;
+        }
+        float o[8];
         // the partner of element e is e +- rot/2; its place among a lane's eight is i or (rot/2 = 4 mod 8) i ^ 4
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int e = e0 + i;
           const int pe = e < half ? e + half : (e < p.rot ? e - half : e);
           const float send = (half & 4) ? v[i ^ 4] : v[i];
-          float partner = __shfl_sync(0xffffffffu, send, pe >> 3, LG);
-          y[i] = e < p.rot ? v[i] * cs[i] + partner * sn[i] : v[i];
+          const float partner = __shfl_sync(0xffffffffu, send, pe >> 3, LG);
+          o[i] = v[i] * ca[i];
+          if (turned[i >> 2]) o[i] = fmaf(partner, cb[i], o[i]);
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          y[g][0] = make_float2(o[4 * g], o[4 * g + 2]);
+          y[g][1] = make_float2(o[4 * g + 1], o[4 * g + 3]);
         }
       }
       const long long off = yb + (long long)h * sd.y_sh + e0;
       if (on && h < sd.heads && SVDQ_INB(p.status, 2 * off, 16, sd.y_extent)) {
         uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          __nv_bfloat162 hv = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-          o[i] = *(uint32_t*)&hv;
+        for (int g = 0; g < 2; ++g) {
+          __nv_bfloat162 h0v = __floats2bfloat162_rn(y[g][0].x, y[g][1].x);
+          __nv_bfloat162 h1v = __floats2bfloat162_rn(y[g][0].y, y[g][1].y);
+          o[2 * g] = *(uint32_t*)&h0v;
+          o[2 * g + 1] = *(uint32_t*)&h1v;
         }
         *(uint4*)(sd.y + off) = make_uint4(o[0], o[1], o[2], o[3]);
       }
@@ -156,13 +223,17 @@ __device__ __forceinline__ void do_side(const NormParams& p, const Side& sd, lon
 }
 
 template <int LG, int PAIRS>
-__global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kThreads, 6) k_qk_norm_rope(const __grid_constant__ NormParams p) {
   pdl_wait();
   const long long n0 = (long long)p.side[0].batch * p.side[0].tokens, n1 = (long long)p.side[1].batch * p.side[1].tokens;
   const long long n = n0 > n1 ? n0 : n1;
   for (long long token = blockIdx.x; token < n; token += gridDim.x) {
-    if (token < n0) do_side<LG, PAIRS>(p, p.side[0], token);
-    if (token < n1) do_side<LG, PAIRS>(p, p.side[1], token);
+    uint4 u0[kUnroll], u1[kUnroll];
+    const Place at0 = place_of(p.side[0], token), at1 = place_of(p.side[1], token);
+    if (token < n0) load_heads<LG>(p, p.side[0], at0, 0, u0);
+    if (token < n1) load_heads<LG>(p, p.side[1], at1, 0, u1);
+    if (token < n0) do_side<LG, PAIRS>(p, p.side[0], token, at0, u0);
+    if (token < n1) do_side<LG, PAIRS>(p, p.side[1], token, at1, u1);
   }
 }
 
