@@ -823,10 +823,11 @@ class Fp8Linear:
     def read_act(self, M: int):
         """Activation codes u8 [M, K] and scales f32 [M, ceil(K/128)] from the workspace (after quantize_act)."""
         ws = self.workspace(M).cpu().numpy()
-        ld, kb = (M + 127) // 128 * 128, (self.K + 127) // 128
+        kb = (self.K + 127) // 128
+        ld = (kb + 3) // 4 * 4
         at = (M * self.K + 1023) // 1024 * 1024
-        scales = ws[at:at + 4 * kb * ld].view(np.float32).reshape(kb, ld)[:, :M]
-        return dict(codes=ws[:M * self.K].reshape(M, self.K).copy(), scales=np.ascontiguousarray(scales.T))
+        scales = ws[at:at + 4 * M * ld].view(np.float32).reshape(M, ld)[:, :kb]
+        return dict(codes=ws[:M * self.K].reshape(M, self.K).copy(), scales=scales.copy())
 
     def __del__(self):
         h = getattr(self, "handle", None)

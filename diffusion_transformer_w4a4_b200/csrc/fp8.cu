@@ -29,7 +29,7 @@ struct svdq_fp8_layer {
   const float* bias;     // [N]
   const float* wscales;  // [NB, KB]
   const uint8_t* wcodes;  // [N, K]
-  CUtensorMap map_w[3];  // boxes of 96, 128 and 64 rows
+  CUtensorMap map_w[3];  // boxes of 256, 128 and 64 rows
 };
 
 namespace svdq {
@@ -40,11 +40,13 @@ constexpr float kFp8Max = 448.f;
 constexpr float kAmaxMin = 0x1p-100f;
 constexpr int kQuantThreads = 256;
 
+// Scales of a row (of X, or of a block of 128 rows of W): one per block of 128 inputs, padded to whole 16 bytes.
+int64_t f8_scale_ld(int64_t K) { return ((K + kBlk - 1) / kBlk + 3) / 4 * 4; }
 struct F8Blob {
   size_t bias, wscales, wcodes, total;
 };
 F8Blob f8_blob_layout(int64_t N, int64_t K) {
-  const int64_t nb = (N + kBlk - 1) / kBlk, kb = (K + kBlk - 1) / kBlk;
+  const int64_t nb = (N + kBlk - 1) / kBlk, kb = f8_scale_ld(K);
   F8Blob b{};
   b.bias = 0;
   b.wscales = align_up((size_t)N * 4, kAlign);
@@ -54,14 +56,12 @@ F8Blob f8_blob_layout(int64_t N, int64_t K) {
 }
 struct F8Ws {
   size_t codes, scales, status, total;
-  int64_t ld;  // columns of the scales
 };
 F8Ws f8_ws_layout(int64_t M, int64_t K) {
   F8Ws w{};
-  w.ld = (M + kBlk - 1) / kBlk * kBlk;
   w.codes = 0;
   w.scales = align_up((size_t)M * K, kAlign);
-  w.status = align_up(w.scales + (size_t)((K + kBlk - 1) / kBlk) * w.ld * 4, kAlign);
+  w.status = align_up(w.scales + (size_t)M * f8_scale_ld(K) * 4, kAlign);
   w.total = w.status + 16;
   return w;
 }
@@ -73,7 +73,7 @@ bool f8_shape_ok(int64_t N, int64_t K) {
 // One block of 128 inputs of one token to 16 lanes.
 __global__ void __launch_bounds__(kQuantThreads) k_fp8_quantize(const uint16_t* __restrict__ x, int64_t M, int K, int KB,
                                                               uint8_t* __restrict__ codes, float* __restrict__ scales,
-                                                              int64_t ld, int* __restrict__ status) {
+                                                              int ld, int* __restrict__ status) {
   pdl_wait();
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;  // the GEMM that follows records errors here
   const int sub = threadIdx.x & 15;
@@ -111,53 +111,189 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp8_quantize(const uint16_t* 
         q[h] = lo | (hi << 16);
       }
       if (SVDQ_INB(status, at, 8, M * K)) *(uint2*)(codes + at) = make_uint2(q[0], q[1]);
-      if (sub == 0 && SVDQ_INB(status, 4 * (j * ld + m), 4, 4 * (int64_t)KB * ld)) scales[j * ld + m] = s;
+      if (sub == 0 && SVDQ_INB(status, 4 * (m * ld + j), 4, 4 * M * ld)) scales[m * ld + j] = s;
     }
   }
 }
 
 // ------------------------------------------------------------------ GEMM
-// PAIR: two CTAs on a 256 x 192 tile (each 128 rows of X and 96 of W a stage, 128 x 192 of the sums).  One CTA
-// alone on 128 x 192 would read 40 KiB for 384 clocks of products, 104 bytes a clock, which the L2 does not give to
-// 148 SMs at once; a pair reads 28 KiB a CTA.
-// A fold costs a warp about three times a tensor-memory latency whatever its width, so a tile's columns go to
-// warpgroups of 64 columns each: 64 sums and 64 loaded columns a thread, three warps to each scheduler at 192.
-template <int BN, bool PAIR>
+// A tile is 128 rows of X by BN of W; warps 0-7 fold (four to a half of the columns, which lies inside one block of 128
+// rows of W), warp 8 loads, warp 9 issues the products (10 and 11 only round the warpgroup out).
+template <int BN>
 struct Tile {
-  static constexpr int kRowsB = PAIR ? BN / 2 : BN;  // rows of W in this CTA's stage
-  static constexpr int kStageA = 128 * kBlk, kStageB = kRowsB * kBlk, kStage = kStageA + kStageB;
-  static constexpr int kStages = BN == 192 ? 7 : (BN == 128 ? 6 : 8);
-  static constexpr int kBufs = BN == 192 ? 2 : 4;  // tensor-memory accumulators in flight
-  static constexpr uint32_t kCols = BN == 192 ? 512 : BN * kBufs;
-  static constexpr int kTileM = PAIR ? 256 : 128;
-  static constexpr int kFoldWarps = BN / 16;  // warps 0.. fold (a warpgroup for 64 columns)
-  static constexpr int kLoadWarp = kFoldWarps, kMmaWarp = kFoldWarps + 1;
-  static constexpr int kThreads = 32 * kFoldWarps + 128;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 512;
+  static constexpr int kStageA = 128 * kBlk, kStageB = BN * kBlk, kStage = kStageA + kStageB;
+  static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
+  static constexpr int kBufs = BN == 256 ? 2 : 4;  // tensor-memory accumulators in flight
+  static constexpr uint32_t kCols = BN * kBufs;
+  static constexpr int kFoldWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
+  static constexpr int kFoldCols = BN / 2;
+  static constexpr int kOutCols = kFoldCols < 64 ? kFoldCols : 64;  // columns that go out together
+  static constexpr int kOut = 32 * kOutCols * 2;                   // their bytes for the 32 rows of a warp
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kFoldWarps * kOut + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
 };
+constexpr int kGemmThreads = 384;
+// A block of 384 threads starts with 168 registers a thread.  At 256 columns a folding thread holds 128 sums and 64
+// columns on their way, so the folding warps take 224 and leave the others 56: 128 * (2 * 224 + 56) = 384 * 168.
+constexpr int kFoldRegs = 224, kOtherRegs = 56;
+static_assert(128 * (2 * kFoldRegs + kOtherRegs) <= 384 * 168, "the split stays within the launch's registers");
 
 struct F8Params {
   int M, N, KB, NB, m_tiles, num_tiles;
-  const float* sx;  // [KB, ld]
-  long long ld;
-  const float* sw;  // [NB, KB]
+  const float* sx;  // [M, ld]
+  const float* sw;  // [NB, ld]
+  int ld;
   const float* bias;
   uint16_t* Y;
   int* status;
   unsigned long long limit;
 };
 struct F8Maps {
-  CUtensorMap a, b;
+  CUtensorMap a, b, y;  // y: 64 columns of 32 rows
 };
 
-template <int BN, bool PAIR>
-__global__ void __launch_bounds__((Tile<BN, PAIR>::kThreads), 1) k_gemm_fp8(const __grid_constant__ F8Maps maps,
+// a += s * (32 or 64 columns of tensor memory from `t`) in one statement: the columns come with one latency, and the
+// registers they pass through stay inside it.
+__device__ __forceinline__ void fold32(uint32_t t, float s, float* a) {
+  asm volatile(
+      "{\n\t.reg .b32 t<32>;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,"
+      "t16,t17,t18,t19,t20,t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      "fma.rn.f32 %0, t0, %33, %0;\n\t"
+      "fma.rn.f32 %1, t1, %33, %1;\n\t"
+      "fma.rn.f32 %2, t2, %33, %2;\n\t"
+      "fma.rn.f32 %3, t3, %33, %3;\n\t"
+      "fma.rn.f32 %4, t4, %33, %4;\n\t"
+      "fma.rn.f32 %5, t5, %33, %5;\n\t"
+      "fma.rn.f32 %6, t6, %33, %6;\n\t"
+      "fma.rn.f32 %7, t7, %33, %7;\n\t"
+      "fma.rn.f32 %8, t8, %33, %8;\n\t"
+      "fma.rn.f32 %9, t9, %33, %9;\n\t"
+      "fma.rn.f32 %10, t10, %33, %10;\n\t"
+      "fma.rn.f32 %11, t11, %33, %11;\n\t"
+      "fma.rn.f32 %12, t12, %33, %12;\n\t"
+      "fma.rn.f32 %13, t13, %33, %13;\n\t"
+      "fma.rn.f32 %14, t14, %33, %14;\n\t"
+      "fma.rn.f32 %15, t15, %33, %15;\n\t"
+      "fma.rn.f32 %16, t16, %33, %16;\n\t"
+      "fma.rn.f32 %17, t17, %33, %17;\n\t"
+      "fma.rn.f32 %18, t18, %33, %18;\n\t"
+      "fma.rn.f32 %19, t19, %33, %19;\n\t"
+      "fma.rn.f32 %20, t20, %33, %20;\n\t"
+      "fma.rn.f32 %21, t21, %33, %21;\n\t"
+      "fma.rn.f32 %22, t22, %33, %22;\n\t"
+      "fma.rn.f32 %23, t23, %33, %23;\n\t"
+      "fma.rn.f32 %24, t24, %33, %24;\n\t"
+      "fma.rn.f32 %25, t25, %33, %25;\n\t"
+      "fma.rn.f32 %26, t26, %33, %26;\n\t"
+      "fma.rn.f32 %27, t27, %33, %27;\n\t"
+      "fma.rn.f32 %28, t28, %33, %28;\n\t"
+      "fma.rn.f32 %29, t29, %33, %29;\n\t"
+      "fma.rn.f32 %30, t30, %33, %30;\n\t"
+      "fma.rn.f32 %31, t31, %33, %31;\n\t"
+      "}"
+      : "+f"(a[0]), "+f"(a[1]), "+f"(a[2]), "+f"(a[3]), "+f"(a[4]), "+f"(a[5]), "+f"(a[6]), "+f"(a[7]),
+        "+f"(a[8]), "+f"(a[9]), "+f"(a[10]), "+f"(a[11]), "+f"(a[12]), "+f"(a[13]), "+f"(a[14]), "+f"(a[15]),
+        "+f"(a[16]), "+f"(a[17]), "+f"(a[18]), "+f"(a[19]), "+f"(a[20]), "+f"(a[21]), "+f"(a[22]), "+f"(a[23]),
+        "+f"(a[24]), "+f"(a[25]), "+f"(a[26]), "+f"(a[27]), "+f"(a[28]), "+f"(a[29]), "+f"(a[30]), "+f"(a[31])
+      : "r"(t), "f"(s)
+      : "memory");
+}
+__device__ __forceinline__ void fold64(uint32_t t, float s, float* a) {
+  asm volatile(
+      "{\n\t.reg .b32 t<64>;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,"
+      "t16,t17,t18,t19,t20,t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31,"
+      "t32,t33,t34,t35,t36,t37,t38,t39,t40,t41,t42,t43,t44,t45,t46,t47,"
+      "t48,t49,t50,t51,t52,t53,t54,t55,t56,t57,t58,t59,t60,t61,t62,t63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t"
+      "fma.rn.f32 %0, t0, %65, %0;\n\t"
+      "fma.rn.f32 %1, t1, %65, %1;\n\t"
+      "fma.rn.f32 %2, t2, %65, %2;\n\t"
+      "fma.rn.f32 %3, t3, %65, %3;\n\t"
+      "fma.rn.f32 %4, t4, %65, %4;\n\t"
+      "fma.rn.f32 %5, t5, %65, %5;\n\t"
+      "fma.rn.f32 %6, t6, %65, %6;\n\t"
+      "fma.rn.f32 %7, t7, %65, %7;\n\t"
+      "fma.rn.f32 %8, t8, %65, %8;\n\t"
+      "fma.rn.f32 %9, t9, %65, %9;\n\t"
+      "fma.rn.f32 %10, t10, %65, %10;\n\t"
+      "fma.rn.f32 %11, t11, %65, %11;\n\t"
+      "fma.rn.f32 %12, t12, %65, %12;\n\t"
+      "fma.rn.f32 %13, t13, %65, %13;\n\t"
+      "fma.rn.f32 %14, t14, %65, %14;\n\t"
+      "fma.rn.f32 %15, t15, %65, %15;\n\t"
+      "fma.rn.f32 %16, t16, %65, %16;\n\t"
+      "fma.rn.f32 %17, t17, %65, %17;\n\t"
+      "fma.rn.f32 %18, t18, %65, %18;\n\t"
+      "fma.rn.f32 %19, t19, %65, %19;\n\t"
+      "fma.rn.f32 %20, t20, %65, %20;\n\t"
+      "fma.rn.f32 %21, t21, %65, %21;\n\t"
+      "fma.rn.f32 %22, t22, %65, %22;\n\t"
+      "fma.rn.f32 %23, t23, %65, %23;\n\t"
+      "fma.rn.f32 %24, t24, %65, %24;\n\t"
+      "fma.rn.f32 %25, t25, %65, %25;\n\t"
+      "fma.rn.f32 %26, t26, %65, %26;\n\t"
+      "fma.rn.f32 %27, t27, %65, %27;\n\t"
+      "fma.rn.f32 %28, t28, %65, %28;\n\t"
+      "fma.rn.f32 %29, t29, %65, %29;\n\t"
+      "fma.rn.f32 %30, t30, %65, %30;\n\t"
+      "fma.rn.f32 %31, t31, %65, %31;\n\t"
+      "fma.rn.f32 %32, t32, %65, %32;\n\t"
+      "fma.rn.f32 %33, t33, %65, %33;\n\t"
+      "fma.rn.f32 %34, t34, %65, %34;\n\t"
+      "fma.rn.f32 %35, t35, %65, %35;\n\t"
+      "fma.rn.f32 %36, t36, %65, %36;\n\t"
+      "fma.rn.f32 %37, t37, %65, %37;\n\t"
+      "fma.rn.f32 %38, t38, %65, %38;\n\t"
+      "fma.rn.f32 %39, t39, %65, %39;\n\t"
+      "fma.rn.f32 %40, t40, %65, %40;\n\t"
+      "fma.rn.f32 %41, t41, %65, %41;\n\t"
+      "fma.rn.f32 %42, t42, %65, %42;\n\t"
+      "fma.rn.f32 %43, t43, %65, %43;\n\t"
+      "fma.rn.f32 %44, t44, %65, %44;\n\t"
+      "fma.rn.f32 %45, t45, %65, %45;\n\t"
+      "fma.rn.f32 %46, t46, %65, %46;\n\t"
+      "fma.rn.f32 %47, t47, %65, %47;\n\t"
+      "fma.rn.f32 %48, t48, %65, %48;\n\t"
+      "fma.rn.f32 %49, t49, %65, %49;\n\t"
+      "fma.rn.f32 %50, t50, %65, %50;\n\t"
+      "fma.rn.f32 %51, t51, %65, %51;\n\t"
+      "fma.rn.f32 %52, t52, %65, %52;\n\t"
+      "fma.rn.f32 %53, t53, %65, %53;\n\t"
+      "fma.rn.f32 %54, t54, %65, %54;\n\t"
+      "fma.rn.f32 %55, t55, %65, %55;\n\t"
+      "fma.rn.f32 %56, t56, %65, %56;\n\t"
+      "fma.rn.f32 %57, t57, %65, %57;\n\t"
+      "fma.rn.f32 %58, t58, %65, %58;\n\t"
+      "fma.rn.f32 %59, t59, %65, %59;\n\t"
+      "fma.rn.f32 %60, t60, %65, %60;\n\t"
+      "fma.rn.f32 %61, t61, %65, %61;\n\t"
+      "fma.rn.f32 %62, t62, %65, %62;\n\t"
+      "fma.rn.f32 %63, t63, %65, %63;\n\t"
+      "}"
+      : "+f"(a[0]), "+f"(a[1]), "+f"(a[2]), "+f"(a[3]), "+f"(a[4]), "+f"(a[5]), "+f"(a[6]), "+f"(a[7]),
+        "+f"(a[8]), "+f"(a[9]), "+f"(a[10]), "+f"(a[11]), "+f"(a[12]), "+f"(a[13]), "+f"(a[14]), "+f"(a[15]),
+        "+f"(a[16]), "+f"(a[17]), "+f"(a[18]), "+f"(a[19]), "+f"(a[20]), "+f"(a[21]), "+f"(a[22]), "+f"(a[23]),
+        "+f"(a[24]), "+f"(a[25]), "+f"(a[26]), "+f"(a[27]), "+f"(a[28]), "+f"(a[29]), "+f"(a[30]), "+f"(a[31]),
+        "+f"(a[32]), "+f"(a[33]), "+f"(a[34]), "+f"(a[35]), "+f"(a[36]), "+f"(a[37]), "+f"(a[38]), "+f"(a[39]),
+        "+f"(a[40]), "+f"(a[41]), "+f"(a[42]), "+f"(a[43]), "+f"(a[44]), "+f"(a[45]), "+f"(a[46]), "+f"(a[47]),
+        "+f"(a[48]), "+f"(a[49]), "+f"(a[50]), "+f"(a[51]), "+f"(a[52]), "+f"(a[53]), "+f"(a[54]), "+f"(a[55]),
+        "+f"(a[56]), "+f"(a[57]), "+f"(a[58]), "+f"(a[59]), "+f"(a[60]), "+f"(a[61]), "+f"(a[62]), "+f"(a[63])
+      : "r"(t), "f"(s)
+      : "memory");
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_constant__ F8Maps maps,
                                                              const __grid_constant__ F8Params p) {
-  using T = Tile<BN, PAIR>;
+  using T = Tile<BN>;
+  constexpr int FC = T::kFoldCols, OC = T::kOutCols;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* stages = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);  // [kStages][A | B]
-  uint64_t* full = (uint64_t*)(stages + T::kStages * T::kStage);
+  uint8_t* sm_out = stages + T::kStages * T::kStage;  // [kFoldWarps][kOut]
+  uint64_t* full = (uint64_t*)(sm_out + T::kFoldWarps * T::kOut);
   uint64_t* empty = full + T::kStages;
   uint64_t* acc_full = empty + T::kStages;   // [kBufs]
   uint64_t* acc_empty = acc_full + T::kBufs;  // [kBufs]
@@ -166,17 +302,14 @@ __global__ void __launch_bounds__((Tile<BN, PAIR>::kThreads), 1) k_gemm_fp8(cons
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   WaitCtl wc{abort_flag, p.status, p.limit};
-  const uint32_t rank = PAIR ? cluster_ctarank() : 0;  // the CTA of rank 0 issues the pair's products
-  const int tile0 = PAIR ? blockIdx.x >> 1 : blockIdx.x, tile_step = PAIR ? gridDim.x >> 1 : gridDim.x;
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) {
-      mbar_init(&full[s], PAIR && rank == 0 ? 2 : 1);  // rank 0 also waits for the other CTA's stage
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < T::kBufs; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], (PAIR ? 2 : 1) * T::kFoldWarps);
+      mbar_init(&acc_empty[b], T::kFoldWarps);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
@@ -186,28 +319,23 @@ __global__ void __launch_bounds__((Tile<BN, PAIR>::kThreads), 1) k_gemm_fp8(cons
   // memory on this SM, so the allocation comes behind it too.
   pdl_wait();
   if (warp == T::kMmaWarp) {
-    if constexpr (PAIR) {
-      tmem_alloc_pair(tmem_slot, T::kCols);
-      tmem_relinquish_pair();
-    } else {
-      tmem_alloc(tmem_slot, T::kCols);
-      tmem_relinquish();
-    }
+    tmem_alloc(tmem_slot, T::kCols);
+    tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();  // both CTAs' barriers and tensor memory are there
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= T::kFoldWarps) {
+    if constexpr (BN == 256) reg_shrink<kOtherRegs>();
     if (warp == T::kLoadWarp && lane == 0) {
       // ---------------------------------------------------------- TMA producer
       prefetch_tmap(&maps.a);
       prefetch_tmap(&maps.b);
       int it = 0;
       bool ok = true;
-      for (int tile = tile0; tile < p.num_tiles && ok; tile += tile_step) {
+      for (int tile = blockIdx.x; tile < p.num_tiles && ok; tile += gridDim.x) {
         const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
         for (int j = 0; j < p.KB; ++j, ++it) {
           const int s = it % T::kStages;
@@ -217,184 +345,178 @@ __global__ void __launch_bounds__((Tile<BN, PAIR>::kThreads), 1) k_gemm_fp8(cons
           }
           uint8_t* st = stages + s * T::kStage;
           mbar_arrive_expect_tx(&full[s], T::kStage);
-          tma_load_2d(&maps.a, &full[s], st, j * kBlk, mt * T::kTileM + (int)rank * 128);
-          tma_load_2d(&maps.b, &full[s], st + T::kStageA, j * kBlk, nt * BN + (int)rank * T::kRowsB);
+          tma_load_2d(&maps.a, &full[s], st, j * kBlk, mt * 128);
+          tma_load_2d(&maps.b, &full[s], st + T::kStageA, j * kBlk, nt * BN);
         }
       }
       // No block leaves with copies in flight, whoever gave up on them.
       for (int j = (it > T::kStages ? it - T::kStages : 0); j < it; ++j)
         mbar_wait_drain(&full[j % T::kStages], (j / T::kStages) & 1, drain_limit(p.limit));
-    } else if (PAIR && rank == 1 && warp == T::kMmaWarp) {
-      // ---------------------------------------------------------- the pair's other CTA: pass on that a stage is loaded
-      if (lane == 0) {
-        int it = 0;
-        bool ok = true;
-        for (int tile = tile0; tile < p.num_tiles && ok; tile += tile_step)
-          for (int j = 0; j < p.KB && ok; ++j, ++it) {
-            const int s = it % T::kStages;
-            ok = timed_wait(&full[s], (it / T::kStages) & 1, wc);
-            if (ok) mbar_arrive_cluster(dsmem_addr(smem_u32(&full[s]), 0));
-          }
-      }
     } else if (warp == T::kMmaWarp) {
       // ---------------------------------------------------------- MMA issuer: one accumulator per block of 128
-      // The whole warp walks the loop (its values then live in uniform registers, where the instruction wants
-      // them) and one lane issues.
-      constexpr uint64_t kDesc = sdesc_const(16, 1024, LAYOUT_SW128);
-      constexpr uint32_t idesc = idesc_e4m3_f32(PAIR ? 256 : 128, BN);
-      const uint32_t first = sdesc_addr(stages);
-      int s = 0, b = 0;
-      uint32_t s_par = 0, b_par = 1;
-      bool ok = true;
-      for (int tile = tile0; tile < p.num_tiles && ok; tile += tile_step) {
-        for (int j = 0; j < p.KB; ++j) {
-          ok = warp_timed_wait(&acc_empty[b], b_par, wc) && warp_timed_wait(&full[s], s_par, wc);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t da = kDesc + first + (uint32_t)(s * (T::kStage >> 4)), db = da + (T::kStageA >> 4);
-          if (elect_one()) {
+      if (elect_one()) {
+        constexpr uint64_t kDesc = sdesc_const(16, 1024, LAYOUT_SW128);
+        constexpr uint32_t idesc = idesc_e4m3_f32(128, BN);
+        const uint64_t first = kDesc + sdesc_addr(stages);
+        int s = 0, b = 0;
+        uint32_t s_par = 0, b_par = 1;
+        bool ok = true;
+        for (int tile = blockIdx.x; tile < p.num_tiles && ok; tile += gridDim.x) {
+          for (int j = 0; j < p.KB; ++j) {
+            ok = timed_wait(&acc_empty[b], b_par, wc) && timed_wait(&full[s], s_par, wc);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t da = first + (uint32_t)(s * (T::kStage >> 4)), db = da + (T::kStageA >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kBlk / 32; ++kk) {  // K = 32 codes (bytes) per instruction
-              if constexpr (PAIR)
-                mma_f8f6f4_pair(tmem + b * BN, da + 2 * kk, db + 2 * kk, idesc, kk != 0 ? 1u : 0u);
-              else
-                mma_f8f6f4(tmem + b * BN, da + 2 * kk, db + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+            for (int kk = 0; kk < kBlk / 32; ++kk)  // K = 32 codes (bytes) per instruction
+              mma_f8f6f4(tmem + b * BN, da + 2 * kk, db + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+            umma_commit(&empty[s]);
+            umma_commit(&acc_full[b]);
+            if (++s == T::kStages) {
+              s = 0;
+              s_par ^= 1;
             }
-            if constexpr (PAIR) {
-              umma_commit_both(&empty[s]);
-              umma_commit_both(&acc_full[b]);
-            } else {
-              umma_commit(&empty[s]);
-              umma_commit(&acc_full[b]);
+            if (++b == T::kBufs) {
+              b = 0;
+              b_par ^= 1;
             }
-          }
-          __syncwarp();
-          if (++s == T::kStages) {
-            s = 0;
-            s_par ^= 1;
-          }
-          if (++b == T::kBufs) {
-            b = 0;
-            b_par ^= 1;
           }
         }
-      }
-      if (elect_one()) {
-        if constexpr (PAIR)
-          umma_commit_pair(mma_done);
-        else
-          umma_commit(mma_done);
+        umma_commit(mma_done);
         mbar_wait_drain(mma_done, 0, drain_limit(p.limit));
       }
       __syncwarp();
     }
   } else {
     // ------------------------------------------------------------ fold and epilogue
+    if constexpr (BN == 256) reg_grow<kFoldRegs>();
     const int q = warp & 3;   // tensor-memory lane quarter
-    const int h = warp >> 2;  // columns 64 h.. of the tile: inside one block of 128 rows of W
-    int it = 0;
+    const int h = warp >> 2;  // column half
+    const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(FC * h);
+    // Scales of this thread's row and this warp's columns in a tile; four blocks of 128 to a load.
+    const float4 *px = nullptr, *pw = nullptr;
+    auto scales_of = [&](int mt, int nt) {
+      const int m = min(mt * 128 + 32 * q + lane, p.M - 1);  // rows past the last are not stored
+      const int nb = min((nt * BN + FC * h) / kBlk, p.NB - 1);  // nor are columns past N
+      px = (const float4*)(p.sx + (long long)m * p.ld);
+      pw = (const float4*)(p.sw + (long long)nb * p.ld);
+    };
+    auto fetch = [&](float4& x, float4& w) {
+      if (SVDQ_INB(p.status, (const char*)px - (const char*)p.sx, 16, 4ll * p.M * p.ld)) x = __ldg(px);
+      if (SVDQ_INB(p.status, (const char*)pw - (const char*)p.sw, 16, 4ll * p.NB * p.ld)) w = __ldg(pw);
+      ++px;
+      ++pw;
+    };
+    int mt = blockIdx.x % p.m_tiles, nt = blockIdx.x / p.m_tiles, mt_next = 0, nt_next = 0;
+    scales_of(mt, nt);
+    int b = 0;
+    uint32_t b_par = 0;
     bool ok = true;
-    for (int tile = tile0; tile < p.num_tiles && ok; tile += tile_step) {
-      const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
-      const int m = mt * T::kTileM + (int)rank * 128 + 32 * q + lane;
-      const int n0 = nt * BN + 64 * h;
-      const int nb = min(n0 / kBlk, p.NB - 1);  // columns past N are not stored
-      const float* sw = p.sw + (long long)nb * p.KB;
-      const bool row = m < p.ld;  // the second CTA's rows can lie past the scales' last column
-      const float* sx = p.sx + m;
-      uint64_t acc[32];  // pairs of columns; the sums start from the bias
+    float4 xn = make_float4(0.f, 0.f, 0.f, 0.f), wn = xn;  // the next four blocks' scales, asked for four folds ahead
+    fetch(xn, wn);
+    for (int tile = blockIdx.x; tile < p.num_tiles && ok; tile += gridDim.x) {
+      const int m0 = mt * 128 + 32 * q;
+      const int n0 = nt * BN + FC * h;
+      // The bias is added at the end; bring it near now.
+      if (8 * lane < FC && n0 + 8 * lane < p.N)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bias + n0 + 8 * lane));
+      float acc[FC];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int n = n0 + 4 * i;
-        float4 b4 = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (n < p.N && SVDQ_INB(p.status, 4ll * n, 16, 4ll * p.N)) b4 = __ldg((const float4*)(p.bias + n));
-        acc[2 * i] = pack2(b4.x, b4.y);
-        acc[2 * i + 1] = pack2(b4.z, b4.w);
-      }
-      // The scales of two blocks ahead: a load is used two folds after it is issued.
-      [[maybe_unused]] const long long sx_extent = 4ll * p.KB * p.ld, sw_extent = 4ll * p.NB * p.KB;  // debug build
-      float xs[2], ws[2];
-      auto fetch = [&](int j, int u) {
-        xs[u] = ws[u] = 0.f;
-        if (row && j < p.KB && SVDQ_INB(p.status, 4 * (j * p.ld + m), 4, sx_extent) &&
-            SVDQ_INB(p.status, 4 * ((long long)nb * p.KB + j), 4, sw_extent)) {
-          xs[u] = sx[j * p.ld];
-          ws[u] = __ldg(sw + j);
+      for (int i = 0; i < FC; ++i) acc[i] = 0.f;
+      for (int j0 = 0; j0 < p.KB; j0 += 4) {
+        const float sc[4] = {xn.x * wn.x, xn.y * wn.y, xn.z * wn.z, xn.w * wn.w};
+        if (j0 + 4 >= p.KB) {  // the next tile's (past the last tile: any place inside)
+          const int next = min(tile + (int)gridDim.x, p.num_tiles - 1);
+          mt_next = next % p.m_tiles;
+          nt_next = next / p.m_tiles;
+          scales_of(mt_next, nt_next);
         }
-      };
+        fetch(xn, wn);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) fetch(u, u);
-      for (int j0 = 0; j0 < p.KB && ok; j0 += 2) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 4; ++u) {
           if (j0 + u >= p.KB) break;
-          const int b = it % T::kBufs;
-          ok = warp_timed_wait(&acc_full[b], (it / T::kBufs) & 1, wc);
-          if (!ok) break;
-          ++it;
+          ok = timed_wait(&acc_full[b], b_par, wc) && ok;
+          __syncwarp();
           tc_fence_after();
-          const float s = xs[u] * ws[u];
-          const uint64_t s2 = pack2(s, s);
-          fetch(j0 + u + 2, u);
-          const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * BN + 64 * h);
-#pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(taddr + c, r);
-            tmem_ld_wait_regs(r);
-            if (c == 32) {  // every column of this accumulator is in registers
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) {
-                if (PAIR)
-                  mbar_arrive_cluster(dsmem_addr(smem_u32(&acc_empty[b]), 0));
-                else
-                  mbar_arrive(&acc_empty[b]);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[c / 2 + i] = fma2(pack2(r[2 * i], r[2 * i + 1]), s2, acc[c / 2 + i]);
+          const uint32_t t = taddr + (uint32_t)(b * BN);
+          if constexpr (FC == 128) {
+            fold64(t, sc[u], acc);
+            fold64(t + 64, sc[u], acc + 64);
+          } else if constexpr (FC == 64) {
+            fold64(t, sc[u], acc);
+          } else {
+            fold32(t, sc[u], acc);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&acc_empty[b]);
+          if (++b == T::kBufs) {
+            b = 0;
+            b_par ^= 1;
           }
         }
+        ok = __all_sync(0xffffffffu, ok);  // an expired wait: its sums are not stored
+        if (!ok) break;
       }
       if (!ok) break;
-      if (m < p.M) {
-        const bool wide = (p.N & 15) == 0 && ((uintptr_t)p.Y & 31) == 0;  // rows of whole 32-byte sectors
+      // A thread has a row, and rows lie far apart in memory: OC columns of the warp's 32 rows go through shared memory
+      // (16-byte pieces, swizzled by the row).  64 columns leave by a bulk tensor store, which the next tile's folds need
+      // not wait for; 32 columns by neighbouring lanes that write a row's neighbouring pieces.
+      constexpr int PIECES = OC / 8;  // of a row
+      uint8_t* mine = sm_out + warp * T::kOut;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int n = n0 + 16 * v;
-          if (n >= p.N) break;
-          uint32_t o[8];
+      for (int c = 0; c < FC; c += OC) {
+        if (OC == 64 && lane == 0) bulk_wait_read<0>();  // the store before has read its source
+        __syncwarp();
+#pragma unroll
+        for (int v = 0; v < PIECES; ++v) {
+          float4 b0 = make_float4(0.f, 0.f, 0.f, 0.f), b1 = b0;
+          if (n0 + c + 8 * v < p.N && SVDQ_INB(p.status, 4ll * (n0 + c + 8 * v), 32, 4ll * p.N)) {
+            b0 = __ldg((const float4*)(p.bias + n0 + c + 8 * v));
+            b1 = __ldg((const float4*)(p.bias + n0 + c + 8 * v) + 1);
+          }
+          const float bb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+          uint32_t o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float2 y0 = unpack2(acc[8 * v + 2 * e]), y1 = unpack2(acc[8 * v + 2 * e + 1]);
-            __nv_bfloat162 h0 = __floats2bfloat162_rn(y0.x, y0.y), h1 = __floats2bfloat162_rn(y1.x, y1.y);
-            o[2 * e] = *(uint32_t*)&h0;
-            o[2 * e + 1] = *(uint32_t*)&h1;
+            __nv_bfloat162 hv = __floats2bfloat162_rn(acc[c + 8 * v + 2 * e] + bb[2 * e],
+                                                      acc[c + 8 * v + 2 * e + 1] + bb[2 * e + 1]);
+            o[e] = *(uint32_t*)&hv;
           }
-          const long long at = (long long)m * p.N + n;
-          if (wide) {
-            if (SVDQ_INB(p.status, 2 * at, 32, 2ll * p.M * p.N)) st_global_32b(p.Y + at, o);
-          } else {
-            if (SVDQ_INB(p.status, 2 * at, 16, 2ll * p.M * p.N))
-              *(uint4*)(p.Y + at) = make_uint4(o[0], o[1], o[2], o[3]);
-            if (n + 8 < p.N && SVDQ_INB(p.status, 2 * at + 16, 16, 2ll * p.M * p.N))
-              *(uint4*)(p.Y + at + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+          *(uint4*)(mine + lane * (OC * 2) + ((v ^ lane) & (PIECES - 1)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        if constexpr (OC == 64) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && m0 < p.M && n0 + c < p.N) {  // rows and columns past the last are clipped
+            tma_store_2d(&maps.y, mine, n0 + c, m0);
+            bulk_commit();
           }
+        } else {
+          __syncwarp();
+          const int piece = lane & (PIECES - 1), n = n0 + c + 8 * piece;
+          constexpr int ROWS = 32 / PIECES;  // rows to an instruction
+#pragma unroll
+          for (int i = 0; i < PIECES; ++i) {
+            const int r = ROWS * i + lane / PIECES;
+            const uint4 y = *(const uint4*)(mine + r * (OC * 2) + ((piece ^ r) & (PIECES - 1)) * 16);
+            const long long at = (long long)(m0 + r) * p.N + n;
+            if (m0 + r < p.M && n < p.N && SVDQ_INB(p.status, 2 * at, 16, 2ll * p.M * p.N)) *(uint4*)(p.Y + at) = y;
+          }
+          __syncwarp();
         }
       }
+      mt = mt_next;
+      nt = nt_next;
     }
+    if (OC == 64 && lane == 0) bulk_wait<0>();
   }
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync();  // neither CTA is needed by the other's products, loads or barriers any more
   if (warp == T::kMmaWarp) {
     tc_fence_after();
-    if constexpr (PAIR)
-      tmem_dealloc_pair(tmem, T::kCols);
-    else
-      tmem_dealloc(tmem, T::kCols);
+    tmem_dealloc(tmem, T::kCols);
   }
 }
 
@@ -405,45 +527,33 @@ int launch_f8_quantize(const svdq_fp8_layer* L, const void* X, int64_t M, uint8_
   const int64_t cap = 16 * (int64_t)device_sm_count(L->device);
   if (grid > cap) grid = cap;
   return launch_pdl(k_fp8_quantize, dim3((unsigned)grid), dim3(kQuantThreads), 0, stream, (const uint16_t*)X, M,
-                    (int)L->K, KB, ws + w.codes, (float*)(ws + w.scales), w.ld, (int*)(ws + w.status)) == cudaSuccess
+                    (int)L->K, KB, ws + w.codes, (float*)(ws + w.scales), (int)f8_scale_ld(L->K), (int*)(ws + w.status)) == cudaSuccess
              ? SVDQ_OK
              : SVDQ_ERR_CUDA;
 }
 
-template <int BN, bool PAIR>
+template <int BN>
 int launch_f8_tile(const svdq_fp8_layer* L, const F8Maps& maps, F8Params& p, cudaStream_t stream) {
-  using T = Tile<BN, PAIR>;
+  using T = Tile<BN>;
   {  // the shared-memory attribute belongs to the kernel on each device: set it once per device
     static std::mutex mu;
     static bool attr_set[64] = {};
     if (L->device < 0 || L->device >= 64) return SVDQ_ERR_CUDA;
     std::lock_guard<std::mutex> lock(mu);
     if (!attr_set[L->device]) {
-      if (cudaFuncSetAttribute(k_gemm_fp8<BN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)T::kSmem) !=
+      if (cudaFuncSetAttribute(k_gemm_fp8<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)T::kSmem) !=
           cudaSuccess)
         return SVDQ_ERR_CUDA;
       attr_set[L->device] = true;
     }
   }
-  p.m_tiles = (p.M + T::kTileM - 1) / T::kTileM;
+  p.m_tiles = (p.M + 127) / 128;
   p.num_tiles = p.m_tiles * ((p.N + BN - 1) / BN);
-  const int slots = device_sm_count(L->device) / (PAIR ? 2 : 1);
-  const int grid = (p.num_tiles < slots ? p.num_tiles : slots) * (PAIR ? 2 : 1);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(T::kThreads);
-  cfg.dynamicSmemBytes = T::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_gemm_fp8<BN, PAIR>, maps, p) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+  const int sms = device_sm_count(L->device);
+  const int grid = p.num_tiles < sms ? p.num_tiles : sms;
+  return launch_pdl(k_gemm_fp8<BN>, dim3((unsigned)grid), dim3(kGemmThreads), T::kSmem, stream, maps, p) == cudaSuccess
+             ? SVDQ_OK
+             : SVDQ_ERR_CUDA;
 }
 
 int launch_f8_gemm(const svdq_fp8_layer* L, int64_t M, void* Y, uint8_t* ws, cudaStream_t stream) {
@@ -459,25 +569,25 @@ int launch_f8_gemm(const svdq_fp8_layer* L, int64_t M, void* Y, uint8_t* ws, cud
   p.KB = (int)((L->K + kBlk - 1) / kBlk);
   p.NB = (int)((L->N + kBlk - 1) / kBlk);
   p.sx = (const float*)(ws + w.scales);
-  p.ld = w.ld;
+  p.ld = (int)f8_scale_ld(L->K);
   p.sw = L->wscales;
   p.bias = L->bias;
   p.Y = (uint16_t*)Y;
   p.status = (int*)(ws + w.status);
   p.limit = wait_limit_cycles();
-  // Rounds of tiles over the SMs times the time of a tile's block: pairs on 256 x 192 where they fill the SMs,
-  // narrower tiles of one CTA where there are too few (a tile's fixed part counts as about 64 columns).
+  // Rounds of tiles over the SMs times the time of a tile's block: the widest tiles where they fill the SMs, narrower
+  // ones where there are too few (a tile's fixed part counts as about 64 columns).
   const int64_t sms = device_sm_count(L->device);
-  auto rounds = [&](int64_t tm, int64_t tn, int64_t slots) {
-    return ((M + tm - 1) / tm * ((L->N + tn - 1) / tn) + slots - 1) / slots;
+  auto cost = [&](int64_t bn) {
+    return ((M + 127) / 128 * ((L->N + bn - 1) / bn) + sms - 1) / sms * (bn + 64);
   };
-  const int64_t cost[3] = {rounds(256, 192, sms / 2) * (192 + 64), rounds(128, 128, sms) * (128 + 64),
-                           rounds(128, 64, sms) * (64 + 64)};
-  const int best = cost[0] <= cost[1] && cost[0] <= cost[2] ? 0 : (cost[1] <= cost[2] ? 1 : 2);
+  const int best = cost(256) <= cost(128) && cost(256) <= cost(64) ? 0 : (cost(128) <= cost(64) ? 1 : 2);
   maps.b = L->map_w[best];
-  return best == 0 ? launch_f8_tile<192, true>(L, maps, p, stream)
-                   : best == 1 ? launch_f8_tile<128, false>(L, maps, p, stream)
-                               : launch_f8_tile<64, false>(L, maps, p, stream);
+  st = encode_tmap_2d(&maps.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, (uint64_t)L->N, (uint64_t)M, (uint64_t)L->N * 2, 64, 32,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != SVDQ_OK) return st;
+  return best == 0 ? launch_f8_tile<256>(L, maps, p, stream)
+                   : best == 1 ? launch_f8_tile<128>(L, maps, p, stream) : launch_f8_tile<64>(L, maps, p, stream);
 }
 
 }  // namespace
@@ -534,7 +644,9 @@ svdq_status svdq_fp8_pack(int64_t N, int64_t K, const uint8_t* wcodes, const flo
   std::memset(blob, 0, b.total);
   float* bf = (float*)(blob + b.bias);
   for (int64_t n = 0; n < N; ++n) bf[n] = bias ? host::bf16_to_f32(bias[n]) : 0.f;
-  std::memcpy(blob + b.wscales, wscales, (size_t)ns * 4);
+  const int64_t kb = (K + kBlk - 1) / kBlk, ld = f8_scale_ld(K);
+  for (int64_t i = 0; i < (N + kBlk - 1) / kBlk; ++i)
+    std::memcpy(blob + b.wscales + (size_t)(i * ld) * 4, wscales + i * kb, (size_t)kb * 4);
   std::memcpy(blob + b.wcodes, wcodes, (size_t)N * K);
   return SVDQ_OK;
 }
@@ -564,7 +676,7 @@ svdq_status svdq_fp8_layer_create(const void* dev_blob, size_t blob_bytes, int64
   L->bias = (const float*)(base + b.bias);
   L->wscales = (const float*)(base + b.wscales);
   L->wcodes = base + b.wcodes;
-  const uint32_t rows[3] = {96, 128, 64};
+  const uint32_t rows[3] = {256, 128, 64};
   for (int i = 0; i < 3; ++i) {
     if (encode_tmap_2d(&L->map_w[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, L->wcodes, (uint64_t)K, (uint64_t)N, (uint64_t)K,
                        kBlk, rows[i], CU_TENSOR_MAP_SWIZZLE_128B) != SVDQ_OK) {

@@ -430,7 +430,8 @@ typedef struct svdq_fp8_layer svdq_fp8_layer; /* opaque host-side handle */
 svdq_status svdq_fp8_prepare(const uint16_t* W, int64_t N, int64_t K, uint8_t* wcodes, float* wscales);
 
 /* Device layout ("fp8 blob"), regions 1024-byte aligned: bias f32 [N] | wscales
- * f32 [ceil(N/128), ceil(K/128)] | wcodes u8 [N, K] row-major.  bias bf16 [N] or
+ * f32 [ceil(N/128), S], S = ceil(K/128) rounded up to a multiple of 4 (padding
+ * zero) | wcodes u8 [N, K] row-major.  bias bf16 [N] or
  * NULL (zeros).  wscales may be any finite, non-negative values (a checkpoint's
  * own); codes other than NaN (0x7F, 0xFF).  Else INVALID_ARG. */
 svdq_status svdq_fp8_packed_size(int64_t N, int64_t K, size_t* bytes);
@@ -447,8 +448,7 @@ void svdq_fp8_layer_destroy(svdq_fp8_layer* layer);
 
 /* Workspace for M tokens (caller device memory, 256-byte aligned): activation
  * codes u8 [M, K] at offset 0 | at the next 1024-byte boundary the activation
- * scales f32 [ceil(K/128), M'], M' = M rounded up to a multiple of 128 (columns
- * >= M unused) | at the next 1024-byte boundary int32 status.  Needs no
+ * scales f32 [M, S] (S as in the blob, the padding unused) | at the next 1024-byte boundary int32 status.  Needs no
  * initialisation: each quantize_act sets the status word to 0. */
 svdq_status svdq_fp8_workspace_size(const svdq_fp8_layer* layer, int64_t M, size_t* bytes);
 

@@ -62,7 +62,7 @@ def test_fp8_pack_layout_and_refusals(lib):
     blob = svdq.svdq_fp8_pack(codes, scales, bias)
     assert blob.size == svdq.svdq_fp8_packed_size(N, K) and blob.size % 1024 == 0
     assert np.array_equal(blob[:4 * N].view(np.float32), oracle.bf16_to_f32(bias))
-    assert np.array_equal(blob[1024:1024 + 24].view(np.float32).reshape(2, 3), scales)
+    assert np.array_equal(blob[1024:1024 + 32].view(np.float32).reshape(2, 4), np.pad(scales, ((0, 0), (0, 1))))
     assert np.array_equal(blob[2048:2048 + N * K].reshape(N, K), codes)
     assert not svdq.svdq_fp8_pack(codes, scales)[:4 * N].any()  # no bias: zeros
     nan_code = codes.copy()
