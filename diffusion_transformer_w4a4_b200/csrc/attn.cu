@@ -124,7 +124,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, bool ma
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       uint32_t r[32];
-      tmem_ld_32(t_s + 32 * k, r);
+      tmem_ld_cols(t_s + 32 * k, r);
 #pragma unroll
       for (int j = 0; j < 32; ++j) r[j] = (w[k] >> j) & 1u ? r[j] : 0xFF800000u;
       tmem_st_32x32b_x32(t_s + 32 * k, r);
@@ -275,7 +275,7 @@ __device__ __forceinline__ int ring_pos(int i, int s, bool is_v, int n) {
 __device__ __forceinline__ void softmax_quarter(uint32_t t_s, uint32_t t_o, int quarter, uint32_t w, float c, int npv,
                                                 bool first, float& m, float& l) {
   uint32_t r[32];
-  tmem_ld_32(t_s + 32 * quarter, r);
+  tmem_ld_cols(t_s + 32 * quarter, r);
   float m4[4] = {m, m, m, m};
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
               uint32_t o[32];
-              if (n > 0) tmem_ld_32(t_o + cc + 32 * hh, o);
+              if (n > 0) tmem_ld_cols(t_o + cc + 32 * hh, o);
               if (empty) {  // whatever O holds there
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0u : o[j];
@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
             uint32_t o[32];
 #pragma unroll
             for (int j = 0; j < 32; ++j) o[j] = 0;
-            if (my > 0) tmem_ld_32(t_o + cc, o);
+            if (my > 0) tmem_ld_cols(t_o + cc, o);
             if (valid) {
 #pragma unroll
               for (int v = 0; v < 8; ++v)

@@ -70,26 +70,39 @@ bool f8_shape_ok(int64_t N, int64_t K) {
 }
 
 // ------------------------------------------------------------------ quantizer
-// One block of 128 inputs of one token to 16 lanes.
+// 16 lanes to a block of 128 inputs of one token, R blocks at a time, all asked for before the first is used: four where
+// there are enough to fill the SMs (4608 x 12288: 44 -> 37 us), one where there are few (the latency of one block).
+template <int R>
 __global__ void __launch_bounds__(kQuantThreads) k_fp8_quantize(const uint16_t* __restrict__ x, int64_t M, int K, int KB,
                                                               uint8_t* __restrict__ codes, float* __restrict__ scales,
                                                               int ld, int* __restrict__ status) {
   pdl_wait();
+  pdl_launch_dependents();  // the GEMM's CTAs may set up and ask for their weights
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;  // the GEMM that follows records errors here
-  const int sub = threadIdx.x & 15;
-  const int64_t blocks = M * KB;
-  // whole warps take a round together (two blocks): the shuffles need every lane
-  for (int64_t i0 = ((int64_t)blockIdx.x * kQuantThreads + (threadIdx.x & ~31)) >> 4; i0 < blocks;
-       i0 += (int64_t)gridDim.x * kQuantThreads >> 4) {
-    const int64_t i = i0 + ((threadIdx.x >> 4) & 1);
-    const int64_t m = i / KB;
-    const int j = (int)(i - m * KB);
+  const int sub = threadIdx.x & 15, step = kQuantThreads / 16;
+  const int64_t i = (int64_t)blockIdx.x * (R * step) + (threadIdx.x >> 4);
+  int64_t m = M <= (1 << 17) ? (int64_t)((uint32_t)i / (uint32_t)KB) : i / KB;  // M KB < 2^31 there
+  int j = (int)(i - m * KB);
+  uint4 u[R];
+  int64_t at[R], sc[R];
+  bool on[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
     const int k = j * kBlk + 8 * sub;
-    const bool on = i < blocks && k < K;
-    const int64_t at = m * K + k;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (on && SVDQ_INB(status, 2 * at, 16, 2 * M * K)) u = __ldcs((const uint4*)(x + at));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    on[r] = m < M && k < K;
+    at[r] = m * K + k;
+    sc[r] = m * ld + j;
+    u[r] = make_uint4(0, 0, 0, 0);
+    if (on[r] && SVDQ_INB(status, 2 * at[r], 16, 2 * M * K)) u[r] = __ldcs((const uint4*)(x + at[r]));
+    j += step;
+    while (j >= KB) {
+      j -= KB;
+      ++m;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const uint32_t w[4] = {u[r].x, u[r].y, u[r].z, u[r].w};
     float v[8], mx = kAmaxMin;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -100,7 +113,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp8_quantize(const uint16_t* 
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float s = __fdiv_rn(mx, kFp8Max), inv = __fdiv_rn(1.f, s);
-    if (on) {
+    if (on[r]) {
       uint32_t q[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -110,8 +123,8 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp8_quantize(const uint16_t* 
                                                      __NV_SATFINITE, __NV_E4M3);
         q[h] = lo | (hi << 16);
       }
-      if (SVDQ_INB(status, at, 8, M * K)) *(uint2*)(codes + at) = make_uint2(q[0], q[1]);
-      if (sub == 0 && SVDQ_INB(status, 4 * (m * ld + j), 4, 4 * M * ld)) scales[m * ld + j] = s;
+      if (SVDQ_INB(status, at[r], 8, M * K)) *(uint2*)(codes + at[r]) = make_uint2(q[0], q[1]);
+      if (sub == 0 && SVDQ_INB(status, 4 * sc[r], 4, 4 * M * ld)) scales[sc[r]] = s;
     }
   }
 }
@@ -139,7 +152,7 @@ constexpr int kFoldRegs = 224, kOtherRegs = 56;
 static_assert(128 * (2 * kFoldRegs + kOtherRegs) <= 384 * 168, "the split stays within the launch's registers");
 
 struct F8Params {
-  int M, N, KB, NB, m_tiles, num_tiles;
+  int M, N, KB, NB, m_tiles, num_tiles, splits;
   const float* sx;  // [M, ld]
   const float* sw;  // [NB, ld]
   int ld;
@@ -520,14 +533,217 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
   }
 }
 
+// ------------------------------------------------------------------ GEMM, few tokens
+// Up to 64 tokens: bound by the weight, which is read once.  The operands change places, so that a tile is 128 rows of W
+// (one block of the weight scales) by BT tokens and no tensor-core row goes to a token that is not there; one thread
+// holds a row's sums for all tokens.  A cluster's CTAs split the inputs where there are fewer tiles than SMs, and join
+// through distributed shared memory in the order of their ranks.  Two CTAs share an SM.  The loads of W do not wait for
+// the quantizer.
+constexpr int kMaxSplit = 8;
+template <int BT>
+struct Few {
+  static constexpr int kStageW = 128 * kBlk, kStage = kStageW + BT * kBlk;
+  static constexpr int kStages = BT == 16 ? 5 : (BT == 32 ? 4 : 3);
+  static constexpr int kBufs = BT == 64 ? 4 : 8;
+  static constexpr uint32_t kCols = BT * kBufs;
+  static constexpr int kTable = BT == 64 ? 24576 : 16384;  // bytes of scales: [block][token]
+  static constexpr int kMaxBlocks = kTable / (4 * BT);
+  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kTable + 512;
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs on an SM");
+  static_assert(BT * 128 * 4 <= kStages * kStage, "partial sums fit the stages");
+};
+constexpr int kFewThreads = 192;  // warps 0-3 fold, 4 loads, 5 issues the products
+
+template <int BT>
+__global__ void __launch_bounds__(kFewThreads, 2) k_gemm_fp8_few(const __grid_constant__ F8Maps maps,
+                                                               const __grid_constant__ F8Params p) {
+  using T = Few<BT>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* stages = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);  // [kStages][W | X]
+  float* table = (float*)(stages + T::kStages * T::kStage);                        // [blocks of this CTA][BT]
+  uint64_t* full = (uint64_t*)((uint8_t*)table + T::kTable);
+  uint64_t* empty = full + T::kStages;
+  uint64_t* acc_full = empty + T::kStages;    // [kBufs]
+  uint64_t* acc_empty = acc_full + T::kBufs;  // [kBufs]
+  uint64_t* mma_done = acc_empty + T::kBufs;
+  uint32_t* tmem_slot = (uint32_t*)(mma_done + 1);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  WaitCtl wc{abort_flag, p.status, p.limit};
+  const int rank = p.splits > 1 ? (int)cluster_ctarank() : 0;
+  const int nt = blockIdx.x / p.splits;
+  const int per = (p.KB + p.splits - 1) / p.splits;
+  const int j_first = min(rank * per, p.KB), blocks = min(per, p.KB - j_first);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < T::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < T::kBufs; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 4);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (warp == 4 && lane == 0) {  // the first stages' weights
+    for (int j = 0; j < min(blocks, T::kStages); ++j) {
+      mbar_arrive_expect_tx(&full[j], T::kStage);
+      tma_load_2d(&maps.b, &full[j], stages + j * T::kStage, (j_first + j) * kBlk, nt * 128);
+    }
+  }
+  pdl_wait();  // the quantizer's codes and scales; tensor memory that an earlier kernel may still need on this SM
+  if (warp == 5) {
+    tmem_alloc(tmem_slot, T::kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  float acc[BT];
+#pragma unroll
+  for (int i = 0; i < BT; ++i) acc[i] = 0.f;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int j = 0;
+      for (; j < blocks; ++j) {
+        const int s = j % T::kStages;
+        uint8_t* st = stages + s * T::kStage;
+        if (j >= T::kStages) {
+          if (!timed_wait(&empty[s], ((j / T::kStages) & 1) ^ 1, wc)) break;
+          mbar_arrive_expect_tx(&full[s], T::kStage);
+          tma_load_2d(&maps.b, &full[s], st, (j_first + j) * kBlk, nt * 128);
+        }
+        tma_load_2d(&maps.a, &full[s], st + T::kStageW, (j_first + j) * kBlk, 0);
+      }
+      // No block leaves with copies in flight, whoever gave up on them.
+      for (int k = (j > T::kStages ? j - T::kStages : 0); k < j; ++k)
+        mbar_wait_drain(&full[k % T::kStages], (k / T::kStages) & 1, drain_limit(p.limit));
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ MMA issuer: one accumulator per block of 128
+    if (elect_one()) {
+      constexpr uint64_t kDesc = sdesc_const(16, 1024, LAYOUT_SW128);
+      constexpr uint32_t idesc = idesc_e4m3_f32(128, BT);
+      const uint64_t first = kDesc + sdesc_addr(stages);
+      for (int j = 0; j < blocks; ++j) {
+        const int s = j % T::kStages, b = j % T::kBufs;
+        if (!timed_wait(&acc_empty[b], ((j / T::kBufs) & 1) ^ 1, wc) ||
+            !timed_wait(&full[s], (j / T::kStages) & 1, wc))
+          break;
+        tc_fence_after();
+        const uint64_t dw = first + (uint32_t)(s * (T::kStage >> 4)), dx = dw + (T::kStageW >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kBlk / 32; ++kk)  // K = 32 codes (bytes) per instruction
+          mma_f8f6f4(tmem + b * BT, dw + 2 * kk, dx + 2 * kk, idesc, kk != 0 ? 1u : 0u);
+        umma_commit(&empty[s]);
+        umma_commit(&acc_full[b]);
+      }
+      umma_commit(mma_done);
+      mbar_wait_drain(mma_done, 0, drain_limit(p.limit));
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ fold
+    for (int i = threadIdx.x; i < blocks * BT; i += 128) {  // s_w s_x of this CTA's blocks
+      const int t = i / blocks, j = i - t * blocks;
+      const long long ax = (long long)t * p.ld + j_first + j, aw = (long long)nt * p.ld + j_first + j;
+      float v = 0.f;
+      if (t < p.M && SVDQ_INB(p.status, 4 * ax, 4, 4ll * p.M * p.ld) &&
+          SVDQ_INB(p.status, 4 * aw, 4, 4ll * p.NB * p.ld))
+        v = p.sx[ax] * __ldg(p.sw + aw);
+      table[j * BT + t] = v;
+    }
+    named_bar_sync(1, 128);
+    const uint32_t taddr = tmem + ((uint32_t)(32 * warp) << 16);
+    for (int j = 0; j < blocks; ++j) {
+      const int b = j % T::kBufs;
+      if (!warp_timed_wait(&acc_full[b], (j / T::kBufs) & 1, wc)) break;
+      tc_fence_after();
+      uint32_t r[BT];
+      tmem_ld_cols(taddr + (uint32_t)(b * BT), r);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[b]);
+#pragma unroll
+      for (int i = 0; i < BT; i += 4) {
+        const float4 sc = *(const float4*)(table + j * BT + i);
+        acc[i] = fmaf(__uint_as_float(r[i]), sc.x, acc[i]);
+        acc[i + 1] = fmaf(__uint_as_float(r[i + 1]), sc.y, acc[i + 1]);
+        acc[i + 2] = fmaf(__uint_as_float(r[i + 2]), sc.z, acc[i + 2]);
+        acc[i + 3] = fmaf(__uint_as_float(r[i + 3]), sc.w, acc[i + 3]);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, T::kCols);
+  }
+  const bool good = *abort_flag == 0;  // after an expired wait nothing is stored
+  if (p.splits == 1) {
+    const int n = nt * 128 + threadIdx.x;
+    if (good && warp < 4 && n < p.N && SVDQ_INB(p.status, 4ll * n, 4, 4ll * p.N)) {
+      const float bias = __ldg(p.bias + n);
+#pragma unroll
+      for (int t = 0; t < BT; ++t) {
+        const long long at = (long long)t * p.N + n;
+        if (t < p.M && SVDQ_INB(p.status, 2 * at, 2, 2ll * p.M * p.N))
+          p.Y[at] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[t] + bias));
+      }
+    }
+    return;
+  }
+  float* part = (float*)stages;  // [BT][128]: every load and product is complete
+  if (warp < 4) {
+#pragma unroll
+    for (int t = 0; t < BT; ++t) part[t * 128 + threadIdx.x] = acc[t];
+  }
+  cluster_sync();
+  if (good) {
+    const uint32_t base = smem_u32(part);
+    for (int u = threadIdx.x * p.splits + rank; u < p.M * 32; u += kFewThreads * p.splits) {
+      const int t = u >> 5, c = 4 * (u & 31), n = nt * 128 + c;
+      float4 x[kMaxSplit];
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r)  // all asked for before the first is used
+        x[r] = r < p.splits ? dsmem_ld_f32x4(dsmem_addr(base + (uint32_t)(t * 128 + c) * 4, r))
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
+      const long long at = (long long)t * p.N + n;
+      if (n < p.N && SVDQ_INB(p.status, 4ll * n, 16, 4ll * p.N) && SVDQ_INB(p.status, 2 * at, 8, 2ll * p.M * p.N)) {
+        float4 y = __ldg((const float4*)(p.bias + n));
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r) {
+          y.x += x[r].x;
+          y.y += x[r].y;
+          y.z += x[r].z;
+          y.w += x[r].w;
+        }
+        __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+        *(uint2*)(p.Y + at) = make_uint2(*(uint32_t*)&lo, *(uint32_t*)&hi);
+      }
+    }
+  }
+  cluster_sync();  // a CTA's shared memory stays until every other has read it
+}
+
 int launch_f8_quantize(const svdq_fp8_layer* L, const void* X, int64_t M, uint8_t* ws, cudaStream_t stream) {
   const F8Ws w = f8_ws_layout(M, L->K);
   const int KB = (int)((L->K + kBlk - 1) / kBlk);
-  int64_t grid = (M * KB + kQuantThreads / 16 - 1) / (kQuantThreads / 16);
-  const int64_t cap = 16 * (int64_t)device_sm_count(L->device);
-  if (grid > cap) grid = cap;
-  return launch_pdl(k_fp8_quantize, dim3((unsigned)grid), dim3(kQuantThreads), 0, stream, (const uint16_t*)X, M,
-                    (int)L->K, KB, ws + w.codes, (float*)(ws + w.scales), (int)f8_scale_ld(L->K), (int*)(ws + w.status)) == cudaSuccess
+  const int64_t rounds = (M * KB + kQuantThreads / 16 - 1) / (kQuantThreads / 16);
+  const bool many = rounds >= 8 * (int64_t)device_sm_count(L->device);
+  const dim3 grid((unsigned)(many ? (rounds + 3) / 4 : rounds));
+  return launch_pdl(many ? k_fp8_quantize<4> : k_fp8_quantize<1>, grid, dim3(kQuantThreads), 0, stream,
+                    (const uint16_t*)X, M, (int)L->K, KB, ws + w.codes, (float*)(ws + w.scales), (int)f8_scale_ld(L->K),
+                    (int*)(ws + w.status)) == cudaSuccess
              ? SVDQ_OK
              : SVDQ_ERR_CUDA;
 }
@@ -556,12 +772,70 @@ int launch_f8_tile(const svdq_fp8_layer* L, const F8Maps& maps, F8Params& p, cud
              : SVDQ_ERR_CUDA;
 }
 
+// Once per device: the shared-memory attribute, and how many clusters of each size are resident at once.
+struct FewFit {
+  bool set = false;
+  int clusters[kMaxSplit + 1] = {};
+};
+template <int BT>
+int launch_f8_few(const svdq_fp8_layer* L, const F8Maps& maps, F8Params& p, cudaStream_t stream) {
+  using T = Few<BT>;
+  static std::mutex mu;
+  static FewFit fits[64];
+  if (L->device < 0 || L->device >= 64) return SVDQ_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = T::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  const int tiles = p.NB;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    FewFit& f = fits[L->device];
+    if (!f.set) {
+      if (cudaFuncSetAttribute(k_gemm_fp8_few<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)T::kSmem) !=
+          cudaSuccess)
+        return SVDQ_ERR_CUDA;
+      cfg.numAttrs = 1;
+      for (int c = 2; c <= kMaxSplit; ++c) {
+        attr[0].val.clusterDim.x = (unsigned)c;
+        cfg.gridDim = dim3((unsigned)(296 * c));
+        if (cudaOccupancyMaxActiveClusters(&f.clusters[c], k_gemm_fp8_few<BT>, &cfg) != cudaSuccess) {
+          cudaGetLastError();
+          f.clusters[c] = 0;
+        }
+      }
+      f.set = true;
+    }
+    // The largest cluster of which one for each tile is resident at once, two blocks of 128 to a CTA at least.
+    p.splits = 1;
+    for (int c = 2; c <= kMaxSplit && 2 * c <= p.KB; ++c)
+      if (tiles <= f.clusters[c]) p.splits = c;
+  }
+  while ((p.KB + p.splits - 1) / p.splits > T::kMaxBlocks) {
+    if (p.splits == kMaxSplit) return -1;  // more inputs than the table of scales holds: the tiles above take them
+    ++p.splits;
+  }
+  cfg.gridDim = dim3((unsigned)(tiles * p.splits));
+  attr[0].val.clusterDim.x = (unsigned)p.splits;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_gemm_fp8_few<BT>, maps, p) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+}
+
 int launch_f8_gemm(const svdq_fp8_layer* L, int64_t M, void* Y, uint8_t* ws, cudaStream_t stream) {
   const F8Ws w = f8_ws_layout(M, L->K);
   F8Maps maps;
   std::memset(&maps, 0, sizeof(maps));
+  const int few = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 0));
   int st = encode_tmap_2d(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, ws + w.codes, (uint64_t)L->K, (uint64_t)M,
-                          (uint64_t)L->K, kBlk, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+                          (uint64_t)L->K, kBlk, few ? (uint32_t)few : 128, CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != SVDQ_OK) return st;
   F8Params p{};
   p.M = (int)M;
@@ -575,6 +849,16 @@ int launch_f8_gemm(const svdq_fp8_layer* L, int64_t M, void* Y, uint8_t* ws, cud
   p.Y = (uint16_t*)Y;
   p.status = (int*)(ws + w.status);
   p.limit = wait_limit_cycles();
+  if (few) {
+    maps.b = L->map_w[1];
+    st = few == 16   ? launch_f8_few<16>(L, maps, p, stream)
+         : few == 32 ? launch_f8_few<32>(L, maps, p, stream)
+                     : launch_f8_few<64>(L, maps, p, stream);
+    if (st != -1) return st;
+    st = encode_tmap_2d(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, ws + w.codes, (uint64_t)L->K, (uint64_t)M,
+                        (uint64_t)L->K, kBlk, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != SVDQ_OK) return st;
+  }
   // Rounds of tiles over the SMs times the time of a tile's block: the widest tiles where they fill the SMs, narrower
   // ones where there are too few (a tile's fixed part counts as about 64 columns).
   const int64_t sms = device_sm_count(L->device);
@@ -698,6 +982,9 @@ svdq_status svdq_fp8_workspace_size(const svdq_fp8_layer* L, int64_t M, size_t* 
 
 static svdq_status f8_check(const svdq_fp8_layer* L, int64_t M, const void* ws, size_t ws_bytes) {
   if (!L || M < 0 || M > (1 << 30) || !ws || ((uintptr_t)ws & 255)) return SVDQ_ERR_INVALID_ARG;
+  // tiles and quantizer CTAs are counted in 31 bits
+  if ((M + 127) / 128 * ((L->N + 63) / 64) > (1 << 30) || M * ((L->K + kBlk - 1) / kBlk) > ((int64_t)1 << 36))
+    return SVDQ_ERR_INVALID_ARG;
   if (ws_bytes < f8_ws_layout(M, L->K).total) return SVDQ_ERR_INVALID_ARG;
   return SVDQ_OK;
 }

@@ -69,7 +69,10 @@ def _check(lin, x, y, qw, sw, b):
 @pytest.mark.parametrize("M,K,N", [
     (1, 16, 8), (1, 128, 128), (2, 144, 136), (3, 3072, 64), (7, 1168, 2312), (16, 2048, 1024), (17, 4096, 264),
     (33, 256, 3072), (64, 400, 520), (65, 1536, 776), (77, 1168, 2312), (127, 128, 1000), (128, 512, 128),
-    (129, 640, 4616), (300, 1152, 4608), (513, 2048, 1032), (1000, 272, 9216), (2100, 512, 2568)])
+    (129, 640, 4616), (300, 1152, 4608), (513, 2048, 1032), (1000, 272, 9216), (2100, 512, 2568),
+    # few tokens: every token tile, clusters of each size, and inputs past what a cluster's table of scales holds
+    (1, 12288, 3072), (15, 640, 136), (18, 6144, 1536), (32, 384, 9224), (48, 8208, 520), (64, 12288, 256),
+    (33, 100096, 8), (5, 32768, 24)])
 def test_parity(M, K, N):
     lin, qw, sw, b = _layer(K, N, M + K + N, bias=N % 16 == 0)
     x = _x(ac.generator(M), M, K)
