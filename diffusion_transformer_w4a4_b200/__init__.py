@@ -13,6 +13,7 @@ steps between a block's projections, take torch tensors [batch, tokens, heads, d
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -199,6 +200,21 @@ def _stream(stream) -> int | None:
 def _stream_of(stream, device) -> int | None:
     """_stream for a known device: the raw handle of its current stream, without a Stream object (about 3 us less)."""
     return _torch()._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
+
+
+def _stream_context(stream):
+    """`stream` (a torch stream or a raw handle) as the current stream."""
+    torch = _torch()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                             torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream))))
+
+
+def _empty_like(x, stream):
+    """An output like x, of the memory of the stream that will write it."""
+    if stream is None:
+        return _torch().empty_like(x)
+    with _stream_context(stream):
+        return _torch().empty_like(x)
 
 
 _torch_module = None
@@ -801,7 +817,8 @@ class Fp8Linear:
         _check_input(x, self.K, device)
         M = x.numel() // self.K
         if out is None:
-            out = torch.empty(M, self.N, dtype=torch.bfloat16, device=device)
+            with contextlib.nullcontext() if stream is None else _stream_context(stream):
+                out = torch.empty(M, self.N, dtype=torch.bfloat16, device=device)
         elif not (out.dtype == torch.bfloat16 and out.device == device and out.is_contiguous()
                   and out.numel() == M * self.N):
             raise ValueError(f"expected a contiguous bf16 output [{M}, {self.N}] on {device}")
@@ -923,7 +940,7 @@ def svdq_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, *, eps=1e-6, rope
         shape = x.shape
         b, s, h, d = shape
         if out is None:
-            out = outs[i] = torch.empty_like(x)
+            out = outs[i] = torch.empty_like(x) if stream is None else _empty_like(x, stream)
             yb, yt, yh, _ = out.stride()
             ya = out.data_ptr(), yb, yt, yh
         else:
@@ -964,7 +981,7 @@ def svdq_cross_attn(q, k, v, *, kv_len=None, kv_mask=None, scale=None, out=None,
     if ks != v.shape or kb != b or kd != d:
         raise ValueError(f"q {tuple(shape)}, k {tuple(ks)}, v {tuple(v.shape)} do not fit")
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q) if stream is None else _empty_like(q, stream)
         oa = out.data_ptr(), *out.stride()[:3]
     else:
         oa = _heads("out", out, device)

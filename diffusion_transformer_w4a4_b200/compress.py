@@ -12,16 +12,17 @@ every numeric step in the library's own host code (svdq_prepare,
 svdq_awq_prepare through the C ABI):
 
   scan(layers, rules)        -> one LayerPlan per layer: svdq_w4a4 / awq_w4a16 /
-                                keep (left in bf16), by name pattern and by the
-                                shapes the kernels accept
+                                fp8_block128 (where the rules ask for it) / keep
+                                (left in bf16), by name pattern and by the shapes
+                                the kernels accept
   calibrate(plan, inputs)    -> per layer, what its preparation needs from its own
                                 inputs: the per-channel max |x| (svdq_w4a4) or a
                                 bounded sample of input rows (awq_w4a16)
   quantize(...)              -> canonical prepared arrays per layer
   pack(path, ...)            -> one file: a JSON header and the canonical arrays,
                                 each 1024-byte aligned
-  load(path) / read_packed   -> device layers (SvdqLinear / AwqLinear) or the
-                                canonical arrays on the host
+  load(path) / read_packed   -> device layers (SvdqLinear / AwqLinear / Fp8Linear) or
+                                the canonical arrays on the host
 
 The file holds the canonical (format-defined) arrays, not the device blobs, so
 a checkpoint survives changes of the kernels' internal layout; `load` re-lays
@@ -35,6 +36,10 @@ scales and for every array its byte offset, byte count, dtype and shape.
 Command line (synthetic model, no checkpoint needed):
   python -m diffusion_transformer_w4a4_b200.compress --synthetic-flux-block \
       --tokens 512 --rank 32 --fmt nvfp4 --out block.svdq
+With --heads 24 the block is calibrated with its attention (else the Q slice stands
+in for it), with --attention fp8 its attention projections become FP8 layers, and
+with --run the packed block is loaded and run on the current GPU, against the dense
+block.
 """
 from __future__ import annotations
 
@@ -52,6 +57,7 @@ ALIGN = 1024
 
 SVDQ = "svdq_w4a4"
 AWQ = "awq_w4a16"
+FP8 = "fp8_block128"
 KEEP = "keep"
 
 # Default target rules for diffusion-transformer layer names, tried in order:
@@ -62,6 +68,14 @@ DEFAULT_RULES = (
     (r"(^|\.)(attn|attention|self_attn|cross_attn)\.", SVDQ),
     (r"(^|\.)(ff|ff_context|mlp|ffn|feed_forward)(\.|$)", SVDQ),
     (r"(^|\.)(to_q|to_k|to_v|to_qkv|qkv|to_out|proj_mlp|proj_out|fc1|fc2|linear1|linear2)(\.|$)", SVDQ),
+)
+
+# The same with the attention projections in 8 bits (FP8, a scale for each block of 128).
+FP8_ATTENTION_RULES = (
+    DEFAULT_RULES[0],
+    (r"(^|\.)(attn|attention|self_attn|cross_attn)\.", FP8),
+    (r"(^|\.)(to_q|to_k|to_v|to_kv|to_qkv|qkv|to_out)(\.|$)", FP8),
+    *DEFAULT_RULES[2:],
 )
 
 
@@ -85,7 +99,7 @@ class LinearSpec:
 @dataclasses.dataclass
 class LayerPlan:
     name: str
-    kind: str  # SVDQ, AWQ or KEEP
+    kind: str  # SVDQ, AWQ, FP8 or KEEP
     N: int
     K: int
     rank: int = 0
@@ -100,6 +114,10 @@ def svdq_shape_ok(N: int, K: int, rank: int) -> bool:
 
 def awq_shape_ok(N: int, K: int) -> bool:
     return K % 64 == 0 and 64 <= K <= 12288 and N >= 1
+
+
+def fp8_shape_ok(N: int, K: int) -> bool:
+    return N % 8 == 0 and N >= 8 and K % 16 == 0 and K >= 16 and N <= 1 << 24 and K <= 1 << 20
 
 
 def scan(layers, rules=DEFAULT_RULES, rank: int = 32, fmt: str = "nvfp4") -> list[LayerPlan]:
@@ -125,6 +143,8 @@ def scan(layers, rules=DEFAULT_RULES, rank: int = 32, fmt: str = "nvfp4") -> lis
                 r = 0
         if kind == AWQ and not awq_shape_ok(N, K):
             kind, why = KEEP, "shape not supported by awq_w4a16"
+        if kind == FP8 and not fp8_shape_ok(N, K):
+            kind, why = KEEP, "shape not supported by fp8_block128"
         plans.append(LayerPlan(spec.name, kind, N, K, r if kind == SVDQ else 0, fmt if kind == SVDQ else "", why))
     return plans
 
@@ -136,7 +156,7 @@ def calibrate(plans, inputs: dict, awq_rows: int = 256) -> dict:
     awq_w4a16 layers (the activation-aware scale search runs on them)."""
     stats = {}
     for p in plans:
-        if p.kind == KEEP:
+        if p.kind in (KEEP, FP8):  # fp8_block128 takes its activation scales from each input
             continue
         x = np.ascontiguousarray(inputs[p.name], np.uint16)
         if x.ndim != 2 or x.shape[1] != p.K:
@@ -151,7 +171,7 @@ def calibrate(plans, inputs: dict, awq_rows: int = 256) -> dict:
 
 def quantize(layers, plans, stats, alpha: float = 0.5) -> dict:
     """Canonical prepared arrays per layer, from the library's host preparation."""
-    from . import svdq_awq_prepare, svdq_prepare
+    from . import svdq_awq_prepare, svdq_fp8_prepare, svdq_prepare
 
     specs = {s.name: s for s in layers}
     out = {}
@@ -161,6 +181,10 @@ def quantize(layers, plans, stats, alpha: float = 0.5) -> dict:
         s = specs[p.name]
         if p.kind == SVDQ:
             out[p.name] = svdq_prepare(s.W, s.bias, stats[p.name], alpha, p.rank, p.fmt)
+        elif p.kind == FP8:
+            codes, scales = svdq_fp8_prepare(s.W)
+            bias = np.zeros(s.N, np.uint16) if s.bias is None else np.ascontiguousarray(s.bias, np.uint16)
+            out[p.name] = dict(N=s.N, K=s.K, wcodes=codes, wscales=scales, bias=bias)
         else:
             out[p.name] = svdq_awq_prepare(s.W, s.bias, stats[p.name])
     return out
@@ -169,15 +193,17 @@ def quantize(layers, plans, stats, alpha: float = 0.5) -> dict:
 _FMT_CODES = {"int4": 1, "nvfp4": 2}  # svdq_format values of include/svdq.h
 _SVDQ_FIELDS = ("lambda_", "inv_lambda", "L1", "L2", "wcodes", "wscales", "bias")
 _AWQ_FIELDS = ("s", "inv_s", "wcodes", "wscales", "bias")
+_FP8_FIELDS = ("wcodes", "wscales", "bias")
 
 
 def _align(n: int) -> int:
     return (n + ALIGN - 1) // ALIGN * ALIGN
 
 
-def pack(path: str, plans, canon: dict, layers=None) -> dict:
+def pack(path: str, plans, canon: dict, layers=None, attention: dict | None = None) -> dict:
     """Write the packed checkpoint; `layers` (optional) also stores the bf16
-    weights of the layers kept in bf16 so the file describes the whole model.
+    weights of the layers kept in bf16 so the file describes the whole model, and
+    `attention` (optional: heads, theta) what a block's attention needs besides.
     Returns the header."""
     specs = {s.name: s for s in (layers or [])}
     entries, blobs = [], []
@@ -200,6 +226,8 @@ def pack(path: str, plans, canon: dict, layers=None) -> dict:
         elif p.kind == AWQ:
             c = canon[p.name]
             e.update(alpha=float(c["alpha"]), arrays={f: add(c[f]) for f in _AWQ_FIELDS})
+        elif p.kind == FP8:
+            e.update(arrays={f: add(canon[p.name][f]) for f in _FP8_FIELDS})
         elif p.name in specs:
             sp = specs[p.name]
             arrays = {"W": add(sp.W)}
@@ -208,6 +236,8 @@ def pack(path: str, plans, canon: dict, layers=None) -> dict:
             e.update(arrays=arrays)
         entries.append(e)
     header = {"format": "svdq pack", "version": VERSION, "align": ALIGN, "layers": entries}
+    if attention is not None:
+        header["attention"] = attention
     hbytes = json.dumps(header).encode()
     base = _align(len(MAGIC) + 8 + len(hbytes))
     with open(path, "wb") as f:
@@ -241,14 +271,16 @@ def read_packed(path: str):
                           g_x=e["g_x"], g_w=e["g_w"])
         elif e["kind"] == AWQ:
             arrays.update(N=e["N"], K=e["K"], alpha=e["alpha"])
+        elif e["kind"] == FP8:
+            arrays.update(N=e["N"], K=e["K"])
         out[e["name"]] = arrays
     return header, out
 
 
 def load(path: str, device=None) -> dict:
-    """Device layers of a packed checkpoint: {name: SvdqLinear | AwqLinear | None}
-    (None for layers kept in bf16)."""
-    from . import AwqLinear, SvdqLinear
+    """Device layers of a packed checkpoint: {name: SvdqLinear | AwqLinear |
+    Fp8Linear | None} (None for layers kept in bf16)."""
+    from . import AwqLinear, Fp8Linear, SvdqLinear
 
     header, canon = read_packed(path)
     layers = {}
@@ -257,18 +289,32 @@ def load(path: str, device=None) -> dict:
             layers[e["name"]] = SvdqLinear(canon[e["name"]], device=device)
         elif e["kind"] == AWQ:
             layers[e["name"]] = AwqLinear(canon[e["name"]], device=device)
+        elif e["kind"] == FP8:
+            c = canon[e["name"]]
+            layers[e["name"]] = Fp8Linear(c["wcodes"], c["wscales"], c["bias"], device=device)
         else:
             layers[e["name"]] = None
     return layers
 
 
+def load_block(path: str, device=None, prefix: str = "transformer_blocks.0."):
+    """attention.FluxBlock of a packed checkpoint that holds its attention's description."""
+    from .attention import FluxBlock
+
+    header, _ = read_packed(path)
+    if "attention" not in header:
+        raise ValueError(f"{path}: packed without its attention (heads)")
+    a = header["attention"]
+    return FluxBlock(load(path, device), int(a["heads"]), float(a["theta"]), prefix)
+
+
 def compress(layers, inputs: dict, path: str, rank: int = 32, fmt: str = "nvfp4", alpha: float = 0.5,
-             rules=DEFAULT_RULES):
+             rules=DEFAULT_RULES, attention: dict | None = None):
     """scan -> calibrate -> quantize -> pack; returns (plans, canonical arrays)."""
     plans = scan(layers, rules, rank, fmt)
     stats = calibrate(plans, inputs)
     canon = quantize(layers, plans, stats, alpha)
-    pack(path, plans, canon, layers)
+    pack(path, plans, canon, layers, attention)
     return plans, canon
 
 
@@ -282,15 +328,40 @@ def _f32_to_bf16_bits(a):
     return ((u + 0x7FFF + ((u >> 16) & 1)) >> 16).astype(np.uint16)
 
 
-def synthetic_flux_block(tokens: int = 512, seed: int = 0, width: int = 3072):
+def dense_attention(qkv_bits, heads: int, theta: float = 10000.0, eps: float = 1e-6):
+    """The block's attention on the host, from and to bf16 bits: RMS norm of each head of q and k, rotation of adjacent
+    pairs by the token's position, softmax(q k^T / sqrt(dim)) v; binary64 with one rounding after the rotation (the
+    kernels' order) and one at the end.  [S, 3 * heads * dim] -> [S, heads * dim]."""
+    S = qkv_bits.shape[0]
+    qkv = _bf16_bits_to_f32(qkv_bits).astype(np.float64).reshape(S, 3, heads, -1)
+    dim = qkv.shape[3]
+    angle = np.arange(S)[:, None] * theta ** (-np.arange(dim // 2) * 2.0 / dim)[None, :]
+    turn = (np.cos(angle) + 1j * np.sin(angle))[:, None, :]
+
+    def norm_turn(x):
+        x = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+        z = (x[..., 0::2] + 1j * x[..., 1::2]) * turn
+        y = np.stack((z.real, z.imag), -1).reshape(x.shape)
+        return _bf16_bits_to_f32(_f32_to_bf16_bits(y.astype(np.float32))).astype(np.float64)
+
+    q, k, v = norm_turn(qkv[:, 0]), norm_turn(qkv[:, 1]), qkv[:, 2]
+    out = np.empty_like(v)
+    for h in range(heads):
+        s = q[:, h] @ k[:, h].T / np.sqrt(dim)
+        p = np.exp(s - s.max(-1, keepdims=True))
+        out[:, h] = (p / p.sum(-1, keepdims=True)) @ v[:, h]
+    return _f32_to_bf16_bits(out.reshape(S, -1).astype(np.float32))
+
+
+def synthetic_flux_block(tokens: int = 512, seed: int = 0, width: int = 3072, heads: int = 0):
     """The linear layers of one synthetic FLUX-style double-stream block (image
     stream) with seeded weights ~ N(0, 0.02^2) and biases ~ N(0, 0.01^2), and
     calibration inputs from a dense bf16 forward of the block's linears on seeded
     tokens ~ N(0, 1) with 0.5 % of the channels scaled x50: the adaLN modulation
     linear (input: a per-sample conditioning vector, batch 2), the fused QKV
-    projection, the attention output projection (its input: the Q slice standing
-    in for the attention output), the MLP up-projection and, after a GELU, the
-    MLP down-projection."""
+    projection, the attention output projection (its input: with `heads`, the
+    attention's output; without, the Q slice standing in for it), the MLP
+    up-projection and, after a GELU, the MLP down-projection."""
     from scipy.special import erf
 
     D = width
@@ -317,12 +388,26 @@ def synthetic_flux_block(tokens: int = 512, seed: int = 0, width: int = 3072):
     mod, qkv, out, up, down = layers
     c = tokens_in(2, D)
     x = tokens_in(tokens, D)
-    a = np.ascontiguousarray(dense(x, qkv)[:, :D])
+    a = dense_attention(dense(x, qkv), heads) if heads else np.ascontiguousarray(dense(x, qkv)[:, :D])
     h_out = dense(a, out)
     g = _bf16_bits_to_f32(dense(h_out, up)).astype(np.float64)
     h_gelu = _f32_to_bf16_bits((0.5 * g * (1.0 + erf(g / np.sqrt(2.0)))).astype(np.float32))
     inputs = {mod.name: c, qkv.name: x, out.name: a, up.name: h_out, down.name: h_gelu}
     return layers, inputs
+
+
+def run_packed_block(path: str, layers, inputs: dict, device=None) -> float:
+    """Load a block packed with its attention, run it on the calibration tokens and return the 2-norm of its output's
+    difference from the dense block's, relative to the dense output."""
+    import torch
+
+    block = load_block(path, device)
+    names = [s.name for s in layers]
+    x = torch.from_numpy(inputs[names[1]].view(np.int16)).view(torch.bfloat16).to(block.up.device)
+    y = block.forward(x[None])[0].float().cpu().numpy().astype(np.float64)
+    down = layers[4]
+    ref = _bf16_bits_to_f32(inputs[down.name]) @ _bf16_bits_to_f32(down.W).T + _bf16_bits_to_f32(down.bias)[None, :]
+    return float(np.linalg.norm(y - ref) / np.linalg.norm(ref))
 
 
 def main(argv=None):
@@ -333,15 +418,24 @@ def main(argv=None):
     ap.add_argument("--rank", type=int, default=32)
     ap.add_argument("--fmt", default="nvfp4", choices=["nvfp4", "int4"])
     ap.add_argument("--alpha", type=float, default=0.5)
+    ap.add_argument("--heads", type=int, default=0, help="calibrate with the attention of this many heads")
+    ap.add_argument("--attention", default="svdq", choices=["svdq", "fp8"], help="attention projections: W4A4 or FP8")
+    ap.add_argument("--run", action="store_true", help="run the packed block on the current GPU (needs --heads)")
     ap.add_argument("--out", required=True)
     a = ap.parse_args(argv)
+    if a.run and (not a.heads or a.fmt != "nvfp4"):
+        ap.error("--run needs --heads and an NVFP4 MLP pair")
     if not a.synthetic_flux_block:
         ap.error("only the synthetic model is built in; use the Python API (compress) for a real one")
-    layers, inputs = synthetic_flux_block(a.tokens, width=a.width)
-    plans, _ = compress(layers, inputs, a.out, a.rank, a.fmt, a.alpha)
+    layers, inputs = synthetic_flux_block(a.tokens, width=a.width, heads=a.heads)
+    rules = FP8_ATTENTION_RULES if a.attention == "fp8" else DEFAULT_RULES
+    plans, _ = compress(layers, inputs, a.out, a.rank, a.fmt, a.alpha, rules,
+                        dict(heads=a.heads, theta=10000.0) if a.heads else None)
     for p in plans:
         print(f"{p.name:45s} {p.kind:10s} {p.K:6d} -> {p.N:6d} rank {p.rank:3d} {p.fmt:6s} ({p.reason})")
     print("wrote", a.out)
+    if a.run:
+        print(f"relative error against the dense block: {run_packed_block(a.out, layers, inputs):.4f}")
 
 
 if __name__ == "__main__":

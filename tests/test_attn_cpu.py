@@ -184,3 +184,47 @@ def test_python_refusals():
         svdq.svdq_qk_norm_rope(q)
     with pytest.raises(ValueError, match="CUDA device"):
         svdq.attn_status("cpu")
+
+
+# ------------------------------------------------------------------------------------------------- compression tool
+def test_fp8_layers_in_the_packed_file(tmp_path):
+    from diffusion_transformer_w4a4_b200 import compress
+
+    layers, inputs = compress.synthetic_flux_block(tokens=32, seed=1, width=256, heads=2)
+    path = str(tmp_path / "b.svdq")
+    plans, canon = compress.compress(layers, inputs, path, rank=16, rules=compress.FP8_ATTENTION_RULES,
+                                     attention=dict(heads=2, theta=10000.0))
+    kinds = {p.name.split("transformer_blocks.0.")[1]: p.kind for p in plans}
+    assert kinds == {"norm1.linear": compress.AWQ, "attn.to_qkv": compress.FP8, "attn.to_out.0": compress.FP8,
+                     "ff.net.0.proj": compress.SVDQ, "ff.net.2": compress.SVDQ}
+    header, back = compress.read_packed(path)
+    assert header["attention"] == dict(heads=2, theta=10000.0)
+    for p in plans:
+        for f, a in back[p.name].items():
+            if isinstance(a, np.ndarray):
+                np.testing.assert_array_equal(a, canon[p.name][f])
+    name = "transformer_blocks.0.attn.to_qkv"
+    assert back[name]["wcodes"].dtype == np.uint8 and back[name]["wscales"].shape == (6, 2)
+    # without the rules and heads the tool does what it did
+    plain, _ = compress.synthetic_flux_block(tokens=32, seed=1, width=256)
+    assert all(np.array_equal(a.W, b.W) for a, b in zip(layers, plain))
+    assert all(p.kind != compress.FP8 for p in compress.scan(plain))
+    bad = [compress.LinearSpec("attn.to_q", np.zeros((12, 24), np.uint16))]
+    assert compress.scan(bad, compress.FP8_ATTENTION_RULES)[0].kind == compress.KEEP
+
+
+def test_dense_attention_of_the_synthetic_block():
+    from diffusion_transformer_w4a4_b200 import compress
+
+    rng = np.random.default_rng(0)
+    S, heads, dim = 37, 3, 16
+    bits = wl.f32_to_bf16_bits(rng.standard_normal((S, 3 * heads * dim)).astype(np.float32))
+    out = compress.dense_attention(bits, heads)
+    t = torch.from_numpy(bits.view(np.int16)).view(torch.bfloat16).view(1, S, 3, heads, dim)
+    table = ac.rope_table(S, dim, "cpu")
+    q, _ = ac.norm_rope(t[:, :, 0], None, 1e-6, table, None, "interleaved")
+    k, _ = ac.norm_rope(t[:, :, 1], None, 1e-6, table, None, "interleaved")
+    o, _ = ac.attention(q.to(torch.bfloat16), k.to(torch.bfloat16), t[:, :, 2], None, None, dim ** -0.5)
+    got = torch.from_numpy(oracle.bf16_to_f32(out)).double().view(S, heads, dim)
+    # a table in binary32 against one in binary64 may round a q or k the other way (2^-8 of it at most)
+    assert ((got - o[0]).abs() <= 2.0 ** -8 * o[0].abs() + 2.0 ** -6 * t[:, :, 2].double().abs().amax()).all()
