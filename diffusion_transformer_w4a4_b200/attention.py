@@ -77,7 +77,7 @@ class SelfAttention:
                           pairs=self.pairs, out_q=q, out_k=k)
         o = svdq_cross_attn(q, k, v, kv_len=kv_len, kv_mask=kv_mask,
                             out=x.new_empty(b, s, self.heads, self.dim))
-        return self.to_out.forward(o.view(b, s, -1)).view(b, s, -1)
+        return self.to_out.forward(o.view(b, s, self.to_out.K)).view(b, s, self.to_out.N)
 
     __call__ = forward
 
@@ -116,7 +116,7 @@ class CrossAttention:
         svdq_qk_norm_rope(q, None, self.q_norm, eps=self.eps, rope=rope, positions=positions, pairs=self.pairs,
                           out_q=q)
         o = svdq_cross_attn(q, k, v, kv_len=kv_len, kv_mask=kv_mask)
-        return self.to_out.forward(o.view(b, s, -1)).view(b, s, -1)
+        return self.to_out.forward(o.view(b, s, self.to_out.K)).view(b, s, self.to_out.N)
 
     __call__ = forward
 
@@ -149,6 +149,6 @@ class FluxBlock:
         with torch.cuda.device(self.up.device):
             svdq_mlp_forward(self.up.handle, self.down.handle, h, b * s, y, self.up.workspace(b * s),
                              self.down.workspace(b * s))
-        return y.view(b, s, -1)
+        return y.view(b, s, self.down.N)
 
     __call__ = forward
