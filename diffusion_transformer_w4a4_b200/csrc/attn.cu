@@ -42,6 +42,7 @@ constexpr int kChunkBytes = 128 * 128;  // 128 rows of 64 bf16
 constexpr int kThreads = 384;           // warps 0-3, 4-7 softmax; 8 loads; 9 products; 10 masked rows of V
 constexpr float kLazy = 8.f;
 constexpr int kMaxSplit = 8;
+constexpr float kLog2E = 1.4426950408889634f;
 
 template <int DC>
 struct Geo {  // DC: 64-wide chunks of the head dimension
@@ -89,10 +90,10 @@ __device__ __forceinline__ float ex2(float x) {
 
 // 2^x of two x <= 126 without the special-function unit, which at 16 results a clock bounds the softmax:
 // x = n + f, n the nearest integer (found by adding 1.5 * 2^23), 2^f by the polynomial of degree 4 with the least
-// relative error on [-1/2, 1/2] (2.7e-6 in binary32, from a Remez exchange), n added to the exponent.
+// relative error on [-1/2, 1/2] (2.7e-6 in binary32, from a Remez exchange), n added to the exponent.  Below -125,
+// where the result would be subnormal or the sum of exponents wrap, it is 0 (a score of -inf has no share at all).
 __device__ __forceinline__ float2 ex2_poly(float2 x) {
-  // smaller ones would need subnormals; 2^-125 adds nothing to a sum that holds 2^-8 or more
-  const uint64_t v = pack2(fmaxf(x.x, -125.f), fmaxf(x.y, -125.f));
+  const uint64_t v = pack2(x.x, x.y);
   const uint64_t magic = pack2(12582912.f, 12582912.f), unmagic = pack2(-12582912.f, -12582912.f);
   const uint64_t t = add2(v, magic);
   const uint64_t f = fma2(add2(t, unmagic), pack2(-1.f, -1.f), v);
@@ -102,14 +103,22 @@ __device__ __forceinline__ float2 ex2_poly(float2 x) {
   y = fma2(y, f, pack2(0.6931217908859253f, 0.6931217908859253f));
   y = fma2(y, f, pack2(0.9999992847442627f, 0.9999992847442627f));
   const float2 yy = unpack2(y), tt = unpack2(t);
-  return make_float2(__uint_as_float(__float_as_uint(yy.x) + (__float_as_uint(tt.x) << 23)),
-                     __uint_as_float(__float_as_uint(yy.y) + (__float_as_uint(tt.y) << 23)));
+  const float a = __uint_as_float(__float_as_uint(yy.x) + (__float_as_uint(tt.x) << 23));
+  const float b = __uint_as_float(__float_as_uint(yy.y) + (__float_as_uint(tt.y) << 23));
+  return make_float2(x.x < -125.f ? 0.f : a, x.y < -125.f ? 0.f : b);
 }
 // Largest of three; NaN if one is NaN.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// c m, which the exponents subtract: 0 for a row without a score above -inf (its exponentials are all 0), and NaN where
+// it is infinite (an infinite or NaN score, or scale times a score past binary32), so that the whole row becomes NaN.
+__device__ __forceinline__ float offset_of(float m, float c) {
+  const float x = m * c;
+  return m == -INFINITY ? 0.f : x + (x - x);
 }
 
 // One tile of one row (a thread each): the row of scores at tensor-memory address t_s becomes P there, m and l and, where
@@ -164,8 +173,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, bool ma
       tmem_st_32x32b_x16(t_o + cc, o);
     }
   }
-  // m - m: an infinite or NaN maximum makes the whole row NaN, as the formula does
-  const float mc = m == -INFINITY ? 0.f : fmaf(m, c, m - m);
+  const float mc = offset_of(m, c);
   const uint64_t c2 = pack2(c, c), nmc2 = pack2(-mc, -mc);
   uint64_t l2[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -298,7 +306,7 @@ __device__ __forceinline__ void softmax_quarter(uint32_t t_s, uint32_t t_o, int 
       tmem_st_32x32b_x16(t_o + cc, o);
     }
   }
-  const float mc = m == -INFINITY ? 0.f : fmaf(m, c, m - m);
+  const float mc = offset_of(m, c);
   uint32_t pr[16];
   float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -924,7 +932,7 @@ extern "C" svdq_status svdq_cross_attn(const svdq_attn_args* a, int32_t* status,
     return SVDQ_ERR_INVALID_ARG;
   if (a->heads < 1 || a->kv_heads < 1 || a->heads > 4096 || a->heads % a->kv_heads != 0) return SVDQ_ERR_INVALID_ARG;
   if (a->dim < 8 || a->dim > 128 || a->dim % 8 != 0) return SVDQ_ERR_INVALID_ARG;
-  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return SVDQ_ERR_INVALID_ARG;
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale * kLog2E)) return SVDQ_ERR_INVALID_ARG;
   if (a->batch == 0 || a->q_tokens == 0) return SVDQ_OK;
   int st = check_heads(a->o, a->batch, a->q_tokens, a->heads, a->dim, true);
   if (st == SVDQ_OK) st = check_heads(a->q, a->batch, a->q_tokens, a->heads, a->dim, false);
@@ -967,7 +975,7 @@ extern "C" svdq_status svdq_cross_attn(const svdq_attn_args* a, int32_t* status,
   p.heads_it = p.hq / p.group;
   p.ksteps = (p.d + 15) / 16;
   p.npv = p.ksteps * 16;
-  p.c = a->scale * 1.4426950408889634f;
+  p.c = a->scale * kLog2E;
   p.kv_len = a->kv_len;
   p.kv_mask = a->kv_mask;
   p.mask_ld = a->batch > 1 ? a->mask_stride : 0;

@@ -516,14 +516,17 @@ typedef struct svdq_attn_args {
   const int32_t* kv_len;  /* i32 [batch]: keys of each sample (clamped to [0, kv_tokens]), or NULL (all) */
   const uint8_t* kv_mask; /* u8 [batch, kv_tokens], nonzero: the key counts; NULL: all.  Both given: both hold */
   int64_t mask_stride;    /* elements between the samples' masks (0: one mask for all) */
-  float scale;            /* > 0, finite; usually 1/sqrt(dim) */
+  float scale;            /* > 0, scale * log2(e) finite; usually 1/sqrt(dim) */
 } svdq_attn_args;
 
 /* O[b,s,h,:] = sum_t p_t V[b,t,h',:] / sum_t p_t, p_t = exp(scale * Q[b,s,h,:].K[b,t,h',:]),
  * over the keys t that count, h' = h / (heads / kv_heads).  Products of bf16 values
  * with binary32 sums, softmax in binary32; p is rounded to bf16 for the product
- * with V.  A row without a key (or whose scores are all -inf) gives 0; keys that
- * do not count have no influence, whatever their K and V hold (NaN included).
+ * with V; a p below 2^-125 of the row's largest counts as 0.  A row without a key
+ * (or whose scores are all -inf) gives 0; keys that do not count have no influence,
+ * whatever their K and V hold (NaN included).  A NaN or +inf score makes its row NaN,
+ * and so does scale * log2(e) * score past binary32; an infinity or NaN in the V of a key
+ * that counts makes that column of the row infinite or NaN.
  * dim % 8 == 0, 8 <= dim <= 128; heads % kv_heads == 0, heads <= 4096; token and
  * batch counts up to 2^30 (batch * heads * ceil(q_tokens / 128) <= 2^30).  kv_tokens may
  * be 0 (k and v are then not read).  `status` is a device int32, zeroed once by the

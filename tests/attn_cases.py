@@ -9,8 +9,9 @@ Bounds, from the roundings the operators document (u = 2^-24, half a binary32 st
   * norm and rotation: the mean of squares carries (dim + 3) u, its root half of that, rsqrt 2 steps, three products
     and the rotation's sum: |dy| <= h |y| + (dim / 2 + 12) u (|a cos| + |c sin|).
   * attention: a score carries (dim + 2) u sum |q k| (truncated: twice that) and the exponent two more roundings of
-    its argument, the exponential 4 u, the sum over keys n u, p rounded to bf16 (h) in the numerator only:
-    |do| <= h |o| + (h + 2 e) sum p |v| / sum p,  e = 2 (dim + 4) u max(scale sum |q k|) + (n + 8) u."""
+    its argument, the exponential 46 u (2.7e-6, the polynomial's largest relative error on its interval; 2 u where the
+    special-function unit computes it), the sum over keys n u, p rounded to bf16 (h) in the numerator only:
+    |do| <= h |o| + (h + 2 e) sum p |v| / sum p,  e = 2 (dim + 4) u max(scale sum |q k|) + (n + 50) u."""
 import math
 
 import torch
@@ -126,7 +127,7 @@ def attention(q, k, v, kv_len, kv_mask, scale):
             qq, kk, vv = q[i, :, h].double(), k[i, keep, h // (hq // hk)].double(), v[i, keep, h // (hq // hk)].double()
             p = torch.softmax(scale * (qq @ kk.t()), -1)
             mag = scale * (qq.abs() @ kk.abs().t()).amax(-1, keepdim=True)
-            e = 2 * (d + 4) * U * mag + (keep.numel() + 8) * U
+            e = 2 * (d + 4) * U * mag + (keep.numel() + 50) * U
             oo = p @ vv
             o[i, :, h] = oo
             bound[i, :, h] = H * oo.abs() + (H + 2 * e) * (p @ vv.abs())

@@ -156,7 +156,7 @@ def _attn_bytes(**kw):
     dict(q=0), dict(q=8), dict(k=0), dict(v=24), dict(o=0), dict(o=4), dict(batch=-1), dict(sq=-1), dict(sk=-1),
     dict(batch=1 << 31), dict(sq=1 << 31), dict(sk=1 << 31), dict(hq=0), dict(hk=0), dict(hq=5), dict(hq=8192, hk=1),
     dict(dim=0), dict(dim=4), dict(dim=60), dict(dim=136), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
-    dict(scale=float("inf")), dict(qs=(4096, 512, 60)), dict(ks=(4096, 512, 56)), dict(ks=(4096, 0, 64)),
+    dict(scale=float("inf")), dict(scale=3e38), dict(qs=(4096, 512, 60)), dict(ks=(4096, 512, 56)), dict(ks=(4096, 0, 64)),
     dict(qs=(4096, 0, 64)), dict(vs=(4096, -512, 64)), dict(os=(4096, 512, 0)), dict(batch=2, os=(0, 512, 64)),
     dict(batch=2, mask=64, mask_ld=-4), dict(kv_len=2),
 ])

@@ -142,6 +142,45 @@ def test_nan_in_a_counting_key_shows():
     assert torch.isfinite(o[1]).all() and torch.isfinite(o[0, :, [0, 2, 3]]).all()
 
 
+@pytest.mark.parametrize("sq,h", [(3, 4), (100, 2), (600, 24)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_scores_of_minus_infinity(sq, h, masked):
+    """Keys with a score of -inf have no share, however large their values; a row of nothing else gives 0."""
+    import torch
+
+    import diffusion_transformer_w4a4_b200 as svdq
+
+    sk, d = 400, 64
+    q = torch.full((2, sq, h, d), 3.0e38, dtype=torch.bfloat16, device="cuda")
+    k = torch.full((2, sk, h, d), -3.0e38, dtype=torch.bfloat16, device="cuda")
+    v = torch.full((2, sk, h, d), 3.0e38, dtype=torch.bfloat16, device="cuda")
+    on = torch.rand(sk, generator=ac.generator(21), device="cuda") < 0.5
+    k[1, on], v[1, on] = 0.0, 1.0  # scores of 0 and values of 1 among them
+    o = svdq.svdq_cross_attn(q, k, v, kv_mask=torch.ones(2, sk, dtype=torch.uint8, device="cuda") if masked else None)
+    assert not o[0].any()
+    assert (o[1] == 1).all()
+
+
+@pytest.mark.parametrize("sq,h", [(3, 4), (100, 2), (600, 24)])
+def test_scores_past_binary32(sq, h):
+    """A score, or scale times a score, past binary32: NaN in its rows, and nothing else."""
+    import torch
+
+    import diffusion_transformer_w4a4_b200 as svdq
+
+    g = ac.generator(22)
+    q, k, v = (ac.bf16(g, 2, n, h, 64) for n in (sq, 300, 300))
+    big = q.abs()
+    big[1], pos = 0.0, k.abs()
+    o = svdq.svdq_cross_attn(big, pos, v, scale=3e37)
+    assert torch.isnan(o[0]).all()
+    ac.check(o[1:], *ac.attention(big[1:], pos[1:], v[1:], None, None, 3e37))
+    k[0, 250], q[:, :, 0] = 3.0e38, 3.0e38  # the first head's rows reach +inf
+    o = svdq.svdq_cross_attn(q, k, v)
+    assert torch.isnan(o[0, :, 0]).all()
+    assert torch.isfinite(o[1, :, 1:]).all()
+
+
 @pytest.mark.parametrize("sq", [3, 600])
 def test_sharp_and_growing_scores(sq):
     """Scores far apart, and rising from tile to tile, so that the running maximum moves often."""
