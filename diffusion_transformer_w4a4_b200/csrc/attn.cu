@@ -27,6 +27,7 @@
 // before the product (0 x NaN would poison it).  Rows without a key give 0.
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -911,6 +912,15 @@ int check_heads(const svdq_heads& h, int64_t batch, int64_t tokens, int64_t head
     span += (size[i] - 1) * stride[i];
     if (span > ((int64_t)1 << 40)) return SVDQ_ERR_INVALID_ARG;
   }
+  // No two places of an output are the same memory: in the order of the strides, each steps over all the ones below it.
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int i, int j) { return stride[i] < stride[j]; });
+  int64_t below = dim;
+  for (int i : order) {
+    if (!out || size[i] <= 1) continue;
+    if (stride[i] < below) return SVDQ_ERR_INVALID_ARG;
+    below += (size[i] - 1) * stride[i];
+  }
   return SVDQ_OK;
 }
 int64_t heads_extent(const svdq_heads& h, int64_t batch, int64_t tokens, int64_t heads, int64_t dim) {
@@ -945,6 +955,8 @@ extern "C" svdq_status svdq_cross_attn(const svdq_attn_args* a, int32_t* status,
     if (st == SVDQ_OK) st = check_heads(a->v, a->batch, a->kv_tokens, a->kv_heads, a->dim, false);
     if (st != SVDQ_OK) return (svdq_status)st;
   }
+  if (a->o.data == a->q.data || (a->kv_tokens > 0 && (a->o.data == a->k.data || a->o.data == a->v.data)))
+    return SVDQ_ERR_INVALID_ARG;
   if (a->kv_mask && a->batch > 1 && a->mask_stride < 0) return SVDQ_ERR_INVALID_ARG;
   if (((uintptr_t)a->kv_len & 3)) return SVDQ_ERR_INVALID_ARG;
   int dev = 0;

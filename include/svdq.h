@@ -476,7 +476,8 @@ svdq_status svdq_fp8_read_status(const svdq_fp8_layer* layer, int64_t M, const v
  * Strides in elements, >= 0, multiples of 8 and at least dim (those of
  * dimensions of size one are ignored); data 16-byte aligned.  A slice of a fused
  * projection's output is such a view.  Where the text below allows a broadcast,
- * its stride is 0. */
+ * its stride is 0.  In an output no two elements are the same memory: in ascending
+ * order each stride is at least the extent of the dimensions below it. */
 typedef struct svdq_heads {
   void* data;
   int64_t stride_batch, stride_token, stride_head;
@@ -511,7 +512,8 @@ svdq_status svdq_qk_norm_rope(const svdq_norm_rope_args* q, const svdq_norm_rope
 typedef struct svdq_attn_args {
   svdq_heads q;           /* [batch, q_tokens, heads, dim] */
   svdq_heads k, v;        /* [batch, kv_tokens, kv_heads, dim]; batch and heads may be broadcast */
-  svdq_heads o;           /* [batch, q_tokens, heads, dim], no overlap with the inputs */
+  svdq_heads o;           /* [batch, q_tokens, heads, dim], no overlap with the inputs (the same data pointer is refused,
+                             other overlap is an error that is not detected) */
   int64_t batch, q_tokens, kv_tokens, heads, kv_heads, dim;
   const int32_t* kv_len;  /* i32 [batch]: keys of each sample (clamped to [0, kv_tokens]), or NULL (all) */
   const uint8_t* kv_mask; /* u8 [batch, kv_tokens], nonzero: the key counts; NULL: all.  Both given: both hold */

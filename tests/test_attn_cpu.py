@@ -124,6 +124,8 @@ def _rope_call(lib, a, k=None, dim=64, rot=0, pairs=0, eps=1e-6, status=None):
     (dict(y=0), {}), (dict(y=20), {}), (dict(batch=-1), {}), (dict(tokens=-1), {}), (dict(heads=-1), {}),
     (dict(batch=1 << 31), {}), (dict(batch=1 << 16, tokens=1 << 16), {}), (dict(xs=(1024, 1024, 12)), {}),
     (dict(xs=(1024, 1024, -128)), {}), (dict(xs=(1024, 1024, 56)), {}), (dict(ys=(1024, 1024, 0)), {}),
+    (dict(tokens=2, ys=(1024, 128, 128)), {}), (dict(tokens=2, ys=(1024, 64, 64)), {}),
+    (dict(tokens=3, batch=2, ys=(2048, 1024, 128)), {}),
     (dict(tokens=2, xs=(1024, 0, 128)), {}), (dict(batch=2, ys=(0, 1024, 128)), {}), (dict(weight=8), {}),
     (dict(rope=8, rows=4), dict(rot=64)), (dict(rope=256, rows=0), dict(rot=64)),
     (dict(rope=256, rows=1, tokens=2), dict(rot=64)), (dict(rope=256, rows=4, pos=2), dict(rot=64)),
@@ -134,6 +136,18 @@ def test_norm_rope_refusals(lib, kw, call):
     if kw is not None:  # as the keys' side too
         good = _rope_bytes()
         assert _rope_call(lib, good, a, **call) == svdq.SVDQ_ERR_INVALID_ARG
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses")
+def test_output_strides_in_any_order(lib):
+    """Views whose elements are all different pass the checks (and stop at the missing device)."""
+    word = ctypes.c_int32()
+    for kw in (dict(os=(4096, 64, 256)), dict(os=(64, 128, 512), batch=2), dict(os=(0, 256, 64)), dict(os=(4096, 512, 128)),
+               dict(batch=2, os=(1984, 512, 64))):  # 64 + 3 * 64 + 3 * 512 = 1792
+        assert lib.svdq_cross_attn(_attn_bytes(**kw), ctypes.byref(word), None) == svdq.SVDQ_ERR_UNSUPPORTED_DEVICE
+    for kw in (dict(tokens=2, ys=(1024, 64, 128)), dict(tokens=2, ys=(0, 128, 64)),
+               dict(tokens=2, x=4096, xs=(0, 128, 64), ys=(0, 128, 64))):
+        assert _rope_call(lib, _rope_bytes(**kw)) == svdq.SVDQ_ERR_UNSUPPORTED_DEVICE
 
 
 def test_norm_rope_empty_is_a_no_op(lib):
@@ -158,7 +172,8 @@ def _attn_bytes(**kw):
     dict(dim=0), dict(dim=4), dict(dim=60), dict(dim=136), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
     dict(scale=float("inf")), dict(scale=3e38), dict(qs=(4096, 512, 60)), dict(ks=(4096, 512, 56)), dict(ks=(4096, 0, 64)),
     dict(qs=(4096, 0, 64)), dict(vs=(4096, -512, 64)), dict(os=(4096, 512, 0)), dict(batch=2, os=(0, 512, 64)),
-    dict(batch=2, mask=64, mask_ld=-4), dict(kv_len=2),
+    dict(batch=2, mask=64, mask_ld=-4), dict(kv_len=2), dict(os=(4096, 64, 64)), dict(os=(4096, 192, 64)),
+    dict(os=(4096, 64, 128)), dict(batch=2, os=(1784, 512, 64)), dict(o=256), dict(o=512), dict(o=1024),
 ])
 def test_attention_refusals(lib, kw):
     word = ctypes.c_int32()
