@@ -7,8 +7,9 @@
 
 The projections are any of the package's layer classes (SvdqLinear, Fp8Linear, W8A8Linear, ...); between them run
 svdq_qk_norm_rope (in place on the projection's output) and svdq_cross_attn.  Everything is enqueued, and every
-intermediate allocated, on `stream` (default: the current stream), and nothing waits.  Like the layers, whose
-workspaces they use, objects here serve one call at a time.
+intermediate allocated, on `stream` (default: the current stream), and nothing waits (but FluxBlock's first call of a
+larger token count, for its rotation table).  Like the layers, whose workspaces they use, objects here serve one call
+at a time.
 """
 from __future__ import annotations
 
@@ -131,12 +132,19 @@ class FluxBlock:
         self.up, self.down = layers[prefix + "ff.net.0.proj"], layers[prefix + "ff.net.2"]
         if svdq_mlp_fusable(self.up.handle, self.down.handle) != SVDQ_OK:
             raise ValueError("the MLP pair's shapes or formats cannot be fused (both NVFP4, static scale)")
-        self.theta, self._tables = theta, {}
+        self.theta, self._ropes = theta, []
 
     def _table(self, tokens: int):
-        t = self._tables.get(tokens)
-        if t is None:
-            t = self._tables[tokens] = rope_table(tokens, self.attention.dim, self.theta, self.up.device)
+        """Cosines and sines of the first `tokens` rows; a longer table than any before is made once, and waited for."""
+        import torch
+
+        t = self._ropes[-1] if self._ropes else None
+        if t is None or t.shape[0] < tokens:
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError(f"no rotation table for {tokens} tokens yet: run the block once before the capture")
+            t = rope_table(tokens, self.attention.dim, self.theta, self.up.device)
+            torch.cuda.current_stream(self.up.device).synchronize()  # before any other stream uses it
+            self._ropes.append(t)  # the shorter ones stay: a captured graph may read them
         return t
 
     @_on_stream

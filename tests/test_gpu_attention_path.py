@@ -165,3 +165,41 @@ def test_refusals():
             bad()
     assert mod(ac.bf16(g, 1, 0, 128), kv).shape == (1, 0, 128)
     assert torch.isfinite(mod(ac.bf16(g, 1, 3, 128), kv)).all()
+
+
+def test_block_table_streams_and_capture(tmp_path):
+    """The rotation table of a larger token count: complete before any stream may read it, never made in a capture."""
+    import torch
+
+    from diffusion_transformer_w4a4_b200 import compress
+
+    layers, inputs = compress.synthetic_flux_block(tokens=100, seed=2, width=768, heads=6)
+    path = str(tmp_path / "block.svdq")
+    compress.compress(layers, inputs, path, rules=compress.FP8_ATTENTION_RULES, attention=dict(heads=6, theta=10000.0))
+    block = compress.load_block(path, "cuda:0")
+    x = torch.from_numpy(inputs[layers[1].name].view(np.int16)).view(torch.bfloat16).cuda()[None]
+    short = x[:, :40].contiguous()
+    y_short = block(short)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y = block(x, stream=side)  # a longer table, on another stream
+    again = block(x)
+    torch.cuda.synchronize()
+    assert torch.equal(y, again)
+    assert torch.equal(y_short, block(short))  # the longer table's first rows are the shorter one's
+    longer = torch.cat((x, x), 1)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="before the capture"):
+        with torch.cuda.graph(graph):
+            block(longer)
+    torch.cuda.synchronize()
+    want = block(longer)
+    graph = torch.cuda.CUDAGraph()
+    out = torch.empty_like(want)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out.copy_(block(longer))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
