@@ -46,6 +46,14 @@ def test_shared_key_heads(hq, hk, sq):
     _run(1, sq, 200, hq, hk, 64)
 
 
+@pytest.mark.parametrize("hq,hk", [(6, 3), (9, 3), (16, 4), (20, 4), (48, 4), (32, 2), (96, 3), (66, 2), (260, 2)])
+@pytest.mark.parametrize("d", [40, 128])
+def test_shared_key_heads_many_rows(hq, hk, d):
+    """Pairs of tiles (256 rows of tokens and heads to each of the 148 SMs at least) whose rows mix tokens and heads:
+    groups that divide a warp's 32 rows, and groups that do not."""
+    _run(2, -(-150 * 256 // (2 * hq)) + 5, 130, hq, hk, d)
+
+
 @pytest.mark.parametrize("sk", [1, 2, 127, 128, 129, 255, 256, 257, 384, 511, 513, 640, 1000, 1536, 2049, 4100])
 @pytest.mark.parametrize("sq", [1, 100])
 def test_key_counts_few_rows(sq, sk):

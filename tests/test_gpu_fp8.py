@@ -203,6 +203,8 @@ def test_refusals():
     raw = torch.empty(4096, dtype=torch.bfloat16, device="cuda")
     for call in (lambda: svdq.svdq_fp8_forward(lin.handle, x, 8, y, ws[:-1]),
                  lambda: svdq.svdq_fp8_forward(lin.handle, x, -1, y, ws),
+                 lambda: svdq.svdq_fp8_forward(lin.handle, x, (1 << 30) + 1, y, ws),  # more tokens than counted
+                 lambda: svdq.svdq_fp8_workspace_size(lin.handle, (1 << 30) + 1),
                  lambda: svdq.svdq_fp8_forward(lin.handle, raw[1:], 8, y, ws),
                  lambda: svdq.svdq_fp8_forward(lin.handle, x, 8, raw[1:], ws),
                  lambda: svdq.svdq_fp8_forward(lin.handle, x, 8, None, ws),
