@@ -124,11 +124,14 @@ __device__ __forceinline__ float offset_of(float m, float c) {
 
 // One tile of one row (a thread each): the row of scores at tensor-memory address t_s becomes P there, m and l and, where
 // the maximum has risen, the row of O at t_o follow.  masked: keys whose bit in w is 0 do not count.  Arrives on
+// A row that is not valid (past the tile's last, where shared memory holds anything) has no say in when the warp rescales:
+// equal calls round alike.
 // `part` when three quarters of P are written (its product starts while the last quarter is computed).
 // The scores are read twice, for the maximum and for the exponentials: a row of 128 in registers leaves too few of
 // the 168 a thread has for the rest, and what then goes through local memory costs more than the second read.
 __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, bool masked, const uint32_t (&w)[4], float c,
-                                             int npv, bool first, float& m, float& l, uint64_t* part, int lane) {
+                                             int npv, bool first, bool valid, float& m, float& l, uint64_t* part,
+                                             int lane) {
   float m4[4] = {m, m, m, m};  // four chains
   if (masked) {  // -inf replaces the scores that do not count, here and for the second read
 #pragma unroll
@@ -160,7 +163,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, bool ma
   tmem_ld_32x32b_x32(t_s, sr[0]);
   if (first) {
     m = mx;
-  } else if (__any_sync(0xffffffffu, !((mx - m) * c <= kLazy))) {  // risen, or NaN
+  } else if (__any_sync(0xffffffffu, valid && !((mx - m) * c <= kLazy))) {  // risen, or NaN
     const float f = mx == -INFINITY ? 1.f : ex2((m - mx) * c);
     m = mx;
     l *= f;
@@ -282,7 +285,7 @@ __device__ __forceinline__ int ring_pos(int i, int s, bool is_v, int n) {
 
 // softmax_tile for QUART: of the tile's keys only those of this warp's lane quarter.
 __device__ __forceinline__ void softmax_quarter(uint32_t t_s, uint32_t t_o, int quarter, uint32_t w, float c, int npv,
-                                                bool first, float& m, float& l) {
+                                                bool first, bool valid, float& m, float& l) {
   uint32_t r[32];
   tmem_ld_cols(t_s + 32 * quarter, r);
   float m4[4] = {m, m, m, m};
@@ -294,7 +297,7 @@ __device__ __forceinline__ void softmax_quarter(uint32_t t_s, uint32_t t_o, int 
   const float mx = max3(m4[0], m4[1], max3(m4[2], m4[3], m4[3]));
   if (first) {
     m = mx;
-  } else if (__any_sync(0xffffffffu, !((mx - m) * c <= kLazy))) {  // risen, or NaN
+  } else if (__any_sync(0xffffffffu, valid && !((mx - m) * c <= kLazy))) {  // risen, or NaN
     const float f = mx == -INFINITY ? 1.f : ex2((m - mx) * c);
     m = mx;
     l *= f;
@@ -608,12 +611,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         if (warp_valid) {
           if constexpr (QUART) {
             const uint32_t wq = masked ? (quarter & 2 ? (quarter & 1 ? w[3] : w[2]) : (quarter & 1 ? w[1] : w[0])) : ~0u;
-            softmax_quarter(t_s, t_o, quarter, wq, p.c, p.npv, i == 0, m, l);
+            softmax_quarter(t_s, t_o, quarter, wq, p.c, p.npv, i == 0, valid, m, l);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_part[st]);
           } else {
-            softmax_tile(t_s, t_o, masked, w, p.c, p.npv, i == 0, m, l, &p_part[st], lane);
+            softmax_tile(t_s, t_o, masked, w, p.c, p.npv, i == 0, valid, m, l, &p_part[st], lane);
           }
         } else {
           tc_fence_before();

@@ -274,6 +274,23 @@ def test_equal_bits_streams_and_graphs(sq, hq):
         assert torch.equal(o, ref)
 
 
+@pytest.mark.parametrize("b,sq,sk,hq,hk,d", [(2, 900, 300, 24, 8, 72), (1, 3, 1030, 6, 2, 64), (2, 100, 700, 3, 1, 64),
+                                             (2, 700, 400, 40, 8, 128)])
+def test_equal_bits_whatever_ran_before(b, sq, sk, hq, hk, d):
+    """Groups of heads that leave rows of a tile unused: what an earlier call left in shared memory changes nothing."""
+    import torch
+
+    import diffusion_transformer_w4a4_b200 as svdq
+
+    g = ac.generator(23)
+    q, k, v = ac.bf16(g, b, sq, hq, d), ac.bf16(g, b, sk, hk, d), ac.bf16(g, b, sk, hk, d)
+    want = svdq.svdq_cross_attn(q, k, v)
+    for spread in (0.0, 1.0, 30.0, 1e4, 1e20):
+        other = ac.bf16(g, 8, 1000, 24, 128, scale=spread)
+        svdq.svdq_cross_attn(other, other, other)  # every SM's shared memory
+        assert torch.equal(want, svdq.svdq_cross_attn(q, k, v))
+
+
 @pytest.mark.parametrize("sq,hq,sk", [(2, 4, 3000), (600, 40, 600)])
 def test_wait_limit_reports_and_recovers(sq, hq, sk):
     import torch
