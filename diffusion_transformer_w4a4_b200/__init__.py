@@ -13,10 +13,8 @@ steps between a block's projections, take torch tensors [batch, tokens, heads, d
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
-import struct
 
 import numpy as np
 
@@ -150,7 +148,7 @@ _EXPORTS = {
                                         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "svdq_fp8_read_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
                                             ctypes.POINTER(ctypes.c_int)]),
-    # the argument structures are passed as packed bytes (see _ROPE_ARGS, _ATTN_ARGS)
+    # the argument structures are passed as bytes (a packed svdq_norm_rope_args, svdq_attn_args)
     "svdq_qk_norm_rope": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_char_p, ctypes.c_int64, ctypes.c_int64,
                                          ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]),
     "svdq_cross_attn": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_void_p]),
@@ -195,11 +193,6 @@ def _stream(stream) -> int | None:
 
         return torch.cuda.current_stream().cuda_stream
     return int(getattr(stream, "cuda_stream", stream))
-
-
-def _stream_of(stream, device) -> int | None:
-    """_stream for a known device: the raw handle of its current stream, without a Stream object (about 3 us less)."""
-    return _torch()._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
 
 
 def _stream_context(stream):
@@ -800,6 +793,7 @@ class Fp8Linear:
         self.blob = torch.from_numpy(svdq_fp8_pack(wcodes, wscales, bias)).to(self.device)
         with torch.cuda.device(self.device):
             self.handle = svdq_fp8_layer_create(self.blob, self.blob.numel(), self.N, self.K)
+        self._handle = self.handle.value
         self._ws = {}
 
     def workspace_size(self, M: int) -> int:
@@ -813,24 +807,18 @@ class Fp8Linear:
         return self._ws[M]
 
     def forward(self, x, out=None, stream=None):
-        torch, device = _torch(), self.device
-        _check_input(x, self.K, device)
-        M = x.numel() // self.K
-        if out is None:
-            with contextlib.nullcontext() if stream is None else _stream_context(stream):
-                out = torch.empty(M, self.N, dtype=torch.bfloat16, device=device)
-        elif not (out.dtype == torch.bfloat16 and out.device == device and out.is_contiguous()
-                  and out.numel() == M * self.N):
-            raise ValueError(f"expected a contiguous bf16 output [{M}, {self.N}] on {device}")
-        ws = self._ws.get(M)
-        if ws is None:
-            ws = self.workspace(M)
-        if torch.cuda.current_device() == device.index:
-            svdq_fp8_forward(self.handle, x, M, out, ws, _stream_of(stream, device))
-        else:
-            with torch.cuda.device(device):
-                svdq_fp8_forward(self.handle, x, M, out, ws, _stream_of(stream, device))
-        return out
+        if stream is not None:
+            if out is None:
+                _check_input(x, self.K, self.device)
+                with _stream_context(stream):
+                    out = _torch().empty(x.numel() // self.K, self.N, dtype=x.dtype, device=self.device)
+            stream = _stream(stream)
+        forward = (_calls_module or _calls()).fp8_forward
+        y = forward(self._handle, self.N, self.K, self.device.index, self._ws, x, out, stream)
+        if y is None:  # the first call with this many tokens
+            self.workspace(x.numel() // self.K)
+            y = forward(self._handle, self.N, self.K, self.device.index, self._ws, x, out, stream)
+        return y
 
     __call__ = forward
 
@@ -854,22 +842,29 @@ class Fp8Linear:
 
 
 # ----------------------------------------------------------------------------- between the projections
-_ROPE_ARGS = struct.Struct("P3qP3q3qPPqP")  # svdq_norm_rope_args
-_ATTN_ARGS = struct.Struct("P3qP3qP3qP3q6qPPqf4x")  # svdq_attn_args
 PAIRS = {"interleaved": 0, "halves": 1}
 _attn_status = {}
 
 
-def _call_on(device, where, fn, *args):
-    """fn(*args), a library call that returns a status, with `device` current."""
-    cuda = _torch().cuda
-    if cuda.current_device() == device.index:
-        st = fn(*args)
-    else:
-        with cuda.device(device):
-            st = fn(*args)
-    if st != SVDQ_OK:
-        raise SvdqError(st, where)
+_calls_module = None
+
+
+def _calls():
+    """The module _marshal.so (tensors to the library's arguments), bound to the loaded library; raises if it was not
+    built (no fallback)."""
+    global _calls_module
+    if _calls_module is None:
+        torch, L = _torch(), lib()
+        try:
+            from . import _marshal as m
+        except ImportError as e:
+            raise RuntimeError("_marshal.so is missing or does not load: build it with "
+                               "`python -m diffusion_transformer_w4a4_b200.build`") from e
+        address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
+        m.bind(address(L.svdq_qk_norm_rope), address(L.svdq_cross_attn), address(L.svdq_fp8_forward), SvdqError,
+               attn_status, torch.OutOfMemoryError)
+        _calls_module = m
+    return _calls_module
 
 
 def attn_status(device=None):
@@ -885,33 +880,8 @@ def attn_status(device=None):
             t = torch.zeros(1, dtype=torch.int32, device=device)
             torch.cuda.current_stream().synchronize()  # before any other stream uses it
         _attn_status[device.index] = t
+        _calls().set_status(device.index, t.data_ptr())
     return t
-
-
-def _status_ptr(status, device):
-    if status is None:
-        t = _attn_status.get(device.index)
-        return (attn_status(device) if t is None else t).data_ptr()
-    _check_aux("status", status, _torch().int32, (1,), device)
-    return status.data_ptr()
-
-
-def _heads(name, t, device):
-    """(pointer, strides of batch, tokens and heads) of a bf16 [batch, tokens, heads, dim] view on `device`."""
-    if t.dtype is not _torch().bfloat16 or t.dim() != 4 or not t.is_cuda:
-        raise ValueError(f"{name}: expected a bf16 CUDA tensor [batch, tokens, heads, dim], got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} on {t.device}, q on {device}")
-    sb, st, sh, sd = t.stride()
-    if sd != 1 and t.shape[3] > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr(), sb, st, sh
-
-
-def _check_aux(name, t, dtype, shape, device):
-    if t.dtype is not dtype or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor {tuple(shape)} on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
 
 
 def svdq_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, *, eps=1e-6, rope=None, positions=None,
@@ -921,50 +891,12 @@ def svdq_qk_norm_rope(q, k=None, q_weight=None, k_weight=None, *, eps=1e-6, rope
     "interleaved" or "halves"): row positions[b, s] (int32 [B,S]), or row s without positions.  Any strided view
     with contiguous heads (a slice of a fused projection's output); out_q / out_k may be q / k themselves.  Returns
     the rotated q, or (q, k)."""
-    torch = _torch()
-    device = q.device
-    table = rows = pos = rot = 0
-    if rope is not None:
-        if rope.dim() != 3 or rope.shape[2] != 2:
-            raise ValueError(f"rope: expected [rows, rot/2, 2], got {tuple(rope.shape)}")
-        _check_aux("rope", rope, torch.float32, rope.shape, device)
-        rows, half, _ = rope.shape
-        table, rot = rope.data_ptr(), 2 * half
-    elif positions is not None:
-        raise ValueError("positions need a rope table")
-    packed = [None, None]
-    outs = [out_q, out_k]
-    for i in (0, 1) if k is not None else (0,):
-        x, w, out = (k, k_weight, out_k) if i else (q, q_weight, out_q)
-        xa = _heads("qk"[i], x, device)
-        shape = x.shape
-        b, s, h, d = shape
-        if out is None:
-            out = outs[i] = torch.empty_like(x) if stream is None else _empty_like(x, stream)
-            yb, yt, yh, _ = out.stride()
-            ya = out.data_ptr(), yb, yt, yh
-        else:
-            ya = _heads("out_" + "qk"[i], out, device)
-            if out.shape != shape:
-                raise ValueError(f"out_{'qk'[i]}: {tuple(out.shape)} for {tuple(shape)}")
-        wp = 0
-        if w is not None:
-            _check_aux("weight of " + "qk"[i], w, torch.bfloat16, (d,), device)
-            wp = w.data_ptr()
-        if i == 0:
-            dim = d
-            if positions is not None:
-                _check_aux("positions", positions, torch.int32, (b, s), device)
-                pos = positions.data_ptr()
-        else:
-            if d != dim:
-                raise ValueError(f"heads of {dim} (q) and {d} (k)")
-            if pos and positions.shape != (b, s):
-                raise ValueError(f"positions {tuple(positions.shape)} for k {tuple(shape)}")
-        packed[i] = _ROPE_ARGS.pack(*xa, *ya, b, s, h, wp, table, rows, pos)
-    _call_on(device, "svdq_qk_norm_rope", lib().svdq_qk_norm_rope, packed[0], packed[1], dim, rot, PAIRS[pairs],
-             eps, _status_ptr(status, device), _stream_of(stream, device))
-    return outs[0] if k is None else (outs[0], outs[1])
+    if stream is not None:
+        out_q = _empty_like(q, stream) if out_q is None else out_q
+        out_k = _empty_like(k, stream) if out_k is None and k is not None else out_k
+        stream = _stream(stream)
+    return (_calls_module or _calls()).qk_norm_rope(q, k, q_weight, k_weight, eps, rope, positions, PAIRS[pairs],
+                                                        out_q, out_k, status, stream)
 
 
 def svdq_cross_attn(q, k, v, *, kv_len=None, kv_mask=None, scale=None, out=None, status=None, stream=None):
@@ -972,33 +904,7 @@ def svdq_cross_attn(q, k, v, *, kv_len=None, kv_mask=None, scale=None, out=None,
     and heads of k and v may be expanded): softmax(scale q k^T) v over the first kv_len[b] keys (int32 [B]) with
     kv_mask[b, t] nonzero (uint8 or bool [B,Sk]).  Rows without a key give 0.  scale defaults to 1/sqrt(D).
     Returns bf16 [B,Sq,H,D]."""
-    torch = _torch()
-    device = q.device
-    qa, ka, va = _heads("q", q, device), _heads("k", k, device), _heads("v", v, device)
-    shape, ks = q.shape, k.shape
-    b, sq, h, d = shape
-    kb, sk, hk, kd = ks
-    if ks != v.shape or kb != b or kd != d:
-        raise ValueError(f"q {tuple(shape)}, k {tuple(ks)}, v {tuple(v.shape)} do not fit")
-    if out is None:
-        out = torch.empty_like(q) if stream is None else _empty_like(q, stream)
-        oa = out.data_ptr(), *out.stride()[:3]
-    else:
-        oa = _heads("out", out, device)
-        if out.shape != shape:
-            raise ValueError(f"out {tuple(out.shape)} for q {tuple(shape)}")
-    lens = mask = mask_ld = 0
-    if kv_len is not None:
-        _check_aux("kv_len", kv_len, torch.int32, (b,), device)
-        lens = kv_len.data_ptr()
-    if kv_mask is not None:
-        if kv_mask.dtype not in (torch.uint8, torch.bool) or kv_mask.device != device or kv_mask.shape != (b, sk) or \
-                (sk > 1 and kv_mask.stride(1) != 1):
-            raise ValueError(f"kv_mask: expected uint8 or bool [{b}, {sk}] on {device}, rows contiguous, got "
-                             f"{kv_mask.dtype} {tuple(kv_mask.shape)} on {kv_mask.device}")
-        mask, mask_ld = kv_mask.data_ptr(), kv_mask.stride(0)
-    args = _ATTN_ARGS.pack(*qa, *ka, *va, *oa, b, sq, sk, h, hk, d, lens, mask, mask_ld,
-                           d ** -0.5 if scale is None else scale)
-    _call_on(device, "svdq_cross_attn", lib().svdq_cross_attn, args, _status_ptr(status, device),
-             _stream_of(stream, device))
-    return out
+    if stream is not None:
+        out = _empty_like(q, stream) if out is None else out
+        stream = _stream(stream)
+    return (_calls_module or _calls()).cross_attn(q, k, v, kv_len, kv_mask, scale, out, status, stream)

@@ -1,9 +1,11 @@
 """Build libsvdq.so (the CUDA library behind include/svdq.h) in-tree with nvcc
-for sm_100a.  Usage: python -m diffusion_transformer_w4a4_b200.build"""
+for sm_100a, and _marshal.so (torch tensors to its arguments) with g++.
+Usage: python -m diffusion_transformer_w4a4_b200.build"""
 from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sys
 
@@ -12,6 +14,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsvdq.so")
 # the bounds-checked debug variant: same sources with -DSVDQ_DEBUG_BOUNDS
 LIB_DEBUG = os.path.join(HERE, "libsvdq_debug.so")
+# the Python module that turns torch tensors into the library's arguments
+MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_SRC = os.path.join(CSRC, "torch", "marshal.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -32,6 +37,7 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     """Compile libsvdq.so (or, with debug=True, libsvdq_debug.so: every kernel's
     self-addressed global accesses bounds-checked, errors in the status word)."""
     lib = LIB_DEBUG if debug else LIB
+    build_marshal(force, verbose)
     if not force and not _stale(lib):
         return lib
     if debug:
@@ -60,6 +66,33 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     subprocess.check_call([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lpthread"])
     os.replace(tmp, lib)
     return lib
+
+
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """Compile _marshal.so against the installed torch and Python."""
+    import sysconfig
+
+    header = os.path.join(HERE, "..", "include", "svdq.h")
+    if not force and os.path.exists(MARSHAL) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in (MARSHAL_SRC, header)):
+        return MARSHAL
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    nvcc = shutil.which(os.environ.get("NVCC", "nvcc"))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc))) if nvcc else "/usr/local/cuda"
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", os.path.dirname(header),
+           *(a for d in inc for a in ("-isystem", d)), MARSHAL_SRC, "-o", tmp, "-L", os.path.join(root, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 if __name__ == "__main__":
