@@ -10,17 +10,23 @@
 // less than 2^kLazy in p (sums and O are binary32, so p up to 2^8 costs no precision).
 //
 // Tiles: 128 rows x 128 keys.  S = Q K^T (tcgen05.mma kind::f16, binary32 in tensor memory); one thread
-// per row takes its S row, writes P as bf16 over it, and P V reads P from tensor memory.  P is rounded
-// to bf16 because the product takes 16-bit operands; its sum l uses the unrounded values.  Two streams
+// per row reads its S row twice (maximum, exponentials), writes P as bf16 over it, and P V reads P from tensor memory.
+// P is rounded to bf16 because the product takes 16-bit operands; its sum l uses the unrounded values.  Two streams
 // of 128 rows run in turn, so that one's products overlap the other's exponentials:
-//   PAIR     many rows: the streams are two query tiles that share the key tiles (each key tile is read
-//            once for 256 rows); persistent, one CTA per SM.
-//   !PAIR    fewer rows: the streams are the even and odd key tiles of one query tile, joined at the end;
-//            and a cluster of up to 8 CTAs splits the keys further and joins through distributed shared
-//            memory, in a fixed order (one launch, no workspace, no atomics).
-//   QUART    (!PAIR) 32 rows at most, as in decoding: the rows lie in all four lane quarters of the tile, and a
-//            quarter's warp takes only its quarter of the keys, so that no warp idles and a tile's exponentials
-//            take a quarter of the time; the other quarters' P is zero there, and the quarters are joined too.
+//   kPairs       the streams are two query tiles that share the key tiles (each key tile is read once for 256 rows);
+//                persistent, one CTA per SM.
+//   kSplitPairs  the same for fewer rows, the keys split over a cluster of up to 8 CTAs that join through distributed
+//                shared memory, in a fixed order (one launch, no workspace, no atomics).
+//   kSingle      the streams are the even and odd key tiles of one query tile, joined at the end; and a cluster splits
+//                the keys further.
+//   kQuarter     kSingle with 32 rows at most, as in decoding: the rows lie in all four lane quarters of the tile, and a
+//                quarter's warp takes only its quarter of the keys, so that no warp idles and a tile's exponentials
+//                take a quarter of the time; the other quarters' P is zero there, and the quarters are joined too.
+// What bounds it: with many rows the chain S -> exponentials -> P -> product, about 3200 clocks for a key tile of both
+// streams against 2048 of products (heads of 128: 24 x 4096 x 4608 in 200 us, 1.16 PFLOP/s); with few rows latency
+// (2 x 24 heads of one token over 4096 keys: 13.9 us, 34 MB of keys and values at 2.4 TB/s).  A quarter of the
+// exponentials are computed by a polynomial, as the special-function unit is the busiest: 24 x 4096 x 4608 in 195-200 us
+// against 217 with none of them, 223 with an eighth and 218 with a half.
 // Rows of a tile are (token, query head of the group) pairs, so heads that share keys share their tiles.
 //
 // Masked keys: scores become -inf by selection, and the masked rows of V are zeroed in shared memory
@@ -50,11 +56,15 @@ struct Geo {  // DC: 64-wide chunks of the head dimension
   static constexpr int kSlots = DC == 2 ? 4 : 8;
   static constexpr int kTile = DC * kChunkBytes;
   static constexpr int kPartLd = 64 * DC + 4;
-  static constexpr int kStage = 8 * 32 * 128;  // PAIR: 64 columns of 32 rows a softmax warp; !PAIR: m and l
+  static constexpr int kStage = 8 * 32 * 128;  // kPairs: 64 columns of 32 rows a softmax warp; else m, l and weights
   static constexpr size_t kSmem = 1024 + (size_t)(2 + kSlots) * kTile + kStage + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
   static_assert(256 * kPartLd * 4 <= (2 + kSlots) * kTile, "partial results fit the query tiles and the ring");
 };
+
+// How the work is spread (see the top): pairs of query tiles, the same with their keys split over a cluster, one query
+// tile with its keys split over the streams and a cluster, and that with a quarter of a tile's keys to a warp.
+enum Mode { kPairs, kSplitPairs, kSingle, kQuarter };
 
 struct AttnParams {
   int sq, sk, hq, hk, d;
@@ -243,15 +253,16 @@ struct Walk {
     len = item < p.items ? raw_len(p, b) : 0;
   }
   __device__ __forceinline__ bool more(const AttnParams& p) const { return item < p.items; }
-  template <bool PAIR>
+  template <int MODE>
   __device__ __forceinline__ Item get(const AttnParams& p, int split) const {
+    constexpr bool PAIR = MODE == kPairs || MODE == kSplitPairs;
     Item it;
     it.b = b;
     it.h = h;
     it.tok0 = rt * p.tok_tile * (PAIR ? 2 : 1);
     it.nkeys = max(0, min(len, p.sk));
     const int n = (it.nkeys + kKeys - 1) / kKeys;
-    if (PAIR) {
+    if (MODE == kPairs) {
       it.t0 = 0;
       it.t1 = n;
     } else {
@@ -331,10 +342,12 @@ __device__ __forceinline__ void softmax_quarter(uint32_t t_s, uint32_t t_o, int 
   tmem_st_wait();
 }
 
-template <bool PAIR, int DC, bool QUART>
+template <int MODE, int DC>
 __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ AttnMaps maps,
                                                       const __grid_constant__ AttnParams p) {
   using G = Geo<DC>;
+  constexpr bool PAIR = MODE == kPairs || MODE == kSplitPairs, QUART = MODE == kQuarter;
+  constexpr bool JOIN = MODE != kPairs;  // results of several CTAs or streams are joined at the end
   constexpr int SLOTS = G::kSlots;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -388,9 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
   const uint32_t tmem = *tmem_slot;  // S0/P0 | S1/P1 | O0 | O1, 128 columns each
 
   const bool fixing = p.kv_len != nullptr || p.kv_mask != nullptr;
-  const int split = PAIR ? 0 : (p.splits > 1 ? (int)cluster_ctarank() : 0);
-  const int item0 = PAIR ? (int)blockIdx.x : (int)blockIdx.x / p.splits;
-  const Walk only(p, item0);  // (!PAIR) the CTA's item, for the join
+  const int split = JOIN && p.splits > 1 ? (int)cluster_ctarank() : 0;
+  const int item0 = JOIN ? (int)blockIdx.x / p.splits : (int)blockIdx.x;
+  const Walk only(p, item0);  // (JOIN) the CTA's item
 
   if (warp == 8) {
     // ------------------------------------------------------------ loads
@@ -414,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
       constexpr int kCopies = QUART ? 4 : 1;
       const uint32_t q_bytes = (uint32_t)(kCopies * DC * 128 * p.group * p.tok_tile);
       for (Walk walk(p, item0); walk.more(p) && ok; walk.step(p)) {
-        const Item it = walk.get<PAIR>(p, split);
+        const Item it = walk.get<MODE>(p, split);
         const int n = it.t1 - it.t0;
         if (n == 0) continue;
         const int kvh = (int)((long long)it.h * p.group * p.hk / p.hq);
@@ -487,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
           if (kk >= k0 && kk < k1) mma_bf16_ts(d, pa + 8 * kk, vd + 128 * kk, idesc_o, first && kk == 0 ? 0u : 1u);
       };
       for (Walk walk(p, item0); walk.more(p) && ok; walk.step(p)) {
-        const Item it = walk.get<PAIR>(p, split);
+        const Item it = walk.get<MODE>(p, split);
         const int n = it.t1 - it.t0;
         if (n == 0) continue;
         const int iters = PAIR ? n : (n + 1) / 2;
@@ -549,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
     int base = 0, fixes = 0;
     bool ok = true;
     for (Walk walk(p, item0); walk.more(p) && ok && fixing; walk.step(p)) {
-      const Item it = walk.get<PAIR>(p, split);
+      const Item it = walk.get<MODE>(p, split);
       const int n = it.t1 - it.t0;
       for (int j = 0; j < n && ok; ++j) {
         const int t = it.t0 + j;
@@ -590,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
     int ns = 0, no = 0;
     bool ok = true;
     for (Walk walk(p, item0); walk.more(p) && ok;) {
-      const Item it = walk.get<PAIR>(p, split);
+      const Item it = walk.get<MODE>(p, split);
       walk.step(p);
       const int n = it.t1 - it.t0;
       if (PAIR && st == 1 && !it.second) continue;
@@ -627,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[st]);
       }
-      if (PAIR) {
+      if (!JOIN) {
         if (!ok) break;
         if (n > 0) {
           ok = warp_timed_wait(&o_full[st], no & 1, wc);
@@ -693,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
         // Parts to be joined: rows of O, not normalised, with m and l, in the place of the query and key tiles (every
         // product of both streams is complete).
         for (int s = 0; s < 2 && ok; ++s)
-          if (s < n) ok = warp_timed_wait(&o_full[s], 0, wc);
+          if (PAIR ? n > 0 && (s == 0 || it.second) : s < n) ok = warp_timed_wait(&o_full[s], 0, wc);
         if (!ok) break;
         tc_fence_after();
         if (warp_valid) {
@@ -719,23 +732,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
     }
   }
 
-  if (PAIR && p.o_tma && warp < 8 && lane == 0) bulk_wait<0>();
+  if (!JOIN && p.o_tma && warp < 8 && lane == 0) bulk_wait<0>();
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (!PAIR) {
+  if (JOIN) {
     // Join of the CTA's parts, four columns of a row to a thread, then of the cluster's CTAs, which share the rows out.
+    // (Pairs of tiles: a part for each row, and only the second step.)
     constexpr int NP = QUART ? 8 : 2, RP = QUART ? 32 : 128;
     const bool good = *abort_flag == 0;
-    const int tok0 = only.rt * p.tok_tile;
-    const int per_row = p.d / 4;
-    const int total = min(p.tok_tile, p.sq - tok0) * p.group * per_row;
+    const int tok0 = only.rt * p.tok_tile * (PAIR ? 2 : 1);
+    const int per_row = p.d / 4, tile_rows = p.tok_tile * p.group;
+    const int total = min(p.tok_tile * (PAIR ? 2 : 1), p.sq - tok0) * p.group * per_row;
     float* part = (float*)smem;
-    float* fm = (float*)(sm_stage + 2048);  // [128] of the CTA
-    float* fl = fm + 128;                   // [128]
+    float* fm = PAIR ? sm_m : (float*)(sm_stage + 2048);  // [128] of the CTA (PAIR: [256])
+    float* fl = PAIR ? sm_l : fm + 128;
     auto store = [&](int row, int col, const float (&o)[4], float ll) {
       const float inv = 1.f / ll;
       uint32_t y[2];
@@ -748,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
       const long long off = (long long)only.b * p.o_sb + (long long)tok * p.o_st + (long long)head * p.o_sh + col;
       if (SVDQ_INB(p.status, 2 * off, 8, p.out_extent)) *(uint2*)(p.out + off) = make_uint2(y[0], y[1]);
     };
-    if (good) {
+    if (!PAIR && good) {
       for (int u = threadIdx.x; u < total; u += kThreads) {
         const int row = u / per_row, col = (u - row * per_row) * 4;
         float f[NP], mm = -INFINITY, ll = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -779,38 +793,76 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
       }
     }
     if (p.splits > 1) {
+      // Rows split, split + splits, ... are this CTA's: first the weights of their parts (2^(c (m_r - m)) / l, so that
+      // the sums need one load an element and part), then the sums, four elements to a thread at once.
+      float* weight = (float*)(sm_stage + 4096);  // [row of this CTA][kMaxSplit]; the first is -1 for a row without a key
+      const int rows = total / per_row, mine = (rows - split + p.splits - 1) / p.splits;
+      const uint32_t a_part = smem_u32(part), a_m = smem_u32(fm), a_l = smem_u32(fl);
+      auto place = [&](int row) { return PAIR && row >= tile_rows ? row - tile_rows + 128 : row; };  // of a row's part
       cluster_sync();
       if (good) {
-        const uint32_t a_part = smem_u32(part), a_m = smem_u32(fm), a_l = smem_u32(fl);
-        for (int u = threadIdx.x * p.splits + split; u < total; u += kThreads * p.splits) {
-          const int row = u / per_row, col = (u - row * per_row) * 4;
-          float fr[kMaxSplit], lr[kMaxSplit];
-          float4 x[kMaxSplit];
+        for (int i = threadIdx.x; i < mine; i += kThreads) {
+          const int at = place(i * p.splits + split);
+          float fr[kMaxSplit], lr[kMaxSplit], mm = -INFINITY, ll = 0.f;
 #pragma unroll
           for (int r = 0; r < kMaxSplit; ++r) {  // all asked for before the first is used
-            if (r < p.splits) {
-              fr[r] = dsmem_ld_f32(dsmem_addr(a_m + 4 * row, r));
-              lr[r] = dsmem_ld_f32(dsmem_addr(a_l + 4 * row, r));
-              x[r] = dsmem_ld_f32x4(dsmem_addr(a_part + (uint32_t)(row * G::kPartLd + col) * 4, r));
-            } else {
-              fr[r] = -INFINITY;
-              lr[r] = 0.f;
-              x[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+            fr[r] = r < p.splits ? dsmem_ld_f32(dsmem_addr(a_m + 4 * at, r)) : -INFINITY;
+            lr[r] = r < p.splits ? dsmem_ld_f32(dsmem_addr(a_l + 4 * at, r)) : 0.f;
           }
-          float mm = -INFINITY, ll = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int r = 0; r < kMaxSplit; ++r) mm = fmaxf(mm, fr[r]);
 #pragma unroll
           for (int r = 0; r < kMaxSplit; ++r) {
-            const float f = fr[r] == -INFINITY ? 0.f : ex2((fr[r] - mm) * p.c);
-            ll = fmaf(lr[r], f, ll);
-            o[0] = fmaf(x[r].x, f, o[0]);
-            o[1] = fmaf(x[r].y, f, o[1]);
-            o[2] = fmaf(x[r].z, f, o[2]);
-            o[3] = fmaf(x[r].w, f, o[3]);
+            fr[r] = fr[r] == -INFINITY ? 0.f : ex2((fr[r] - mm) * p.c);
+            ll = fmaf(lr[r], fr[r], ll);
           }
-          store(row, col, o, ll);
+          const float inv = 1.f / ll;
+#pragma unroll
+          for (int r = 0; r < kMaxSplit; ++r) weight[i * kMaxSplit + r] = ll == 0.f ? -1.f : fr[r] * inv;
+        }
+      }
+      __syncthreads();
+      if (good) {
+        constexpr int U = QUART ? 1 : 4, B = QUART ? kMaxSplit : 2;  // elements, and parts of each, asked for at once
+        for (int u0 = threadIdx.x; u0 < mine * per_row; u0 += U * kThreads) {
+          int row[U], col[U], i[U];
+          uint32_t from[U];
+          float4 o[U];
+#pragma unroll
+          for (int j = 0; j < U; ++j) {
+            const int u = min(u0 + j * kThreads, mine * per_row - 1);
+            i[j] = u / per_row;
+            col[j] = (u - i[j] * per_row) * 4;
+            row[j] = i[j] * p.splits + split;
+            from[j] = a_part + (uint32_t)(place(row[j]) * G::kPartLd + col[j]) * 4;
+            o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          for (int r0 = 0; r0 < p.splits; r0 += B) {
+            float4 x[B][U];
+#pragma unroll
+            for (int r = 0; r < B; ++r)
+#pragma unroll
+              for (int j = 0; j < U; ++j)
+                if (r0 + r < p.splits) x[r][j] = dsmem_ld_f32x4(dsmem_addr(from[j], r0 + r));
+#pragma unroll
+            for (int r = 0; r < B; ++r) {
+              if (r0 + r >= p.splits) break;
+#pragma unroll
+              for (int j = 0; j < U; ++j) {
+                const float f = weight[i[j] * kMaxSplit + r0 + r];
+                o[j].x = fmaf(x[r][j].x, f, o[j].x);
+                o[j].y = fmaf(x[r][j].y, f, o[j].y);
+                o[j].z = fmaf(x[r][j].z, f, o[j].z);
+                o[j].w = fmaf(x[r][j].w, f, o[j].w);
+              }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < U; ++j) {
+            const float y[4] = {o[j].x, o[j].y, o[j].z, o[j].w};
+            if (u0 + j * kThreads < mine * per_row)
+              store(row[j], col[j], y, weight[i[j] * kMaxSplit] < 0.f ? 0.f : 1.f);
+          }
         }
       }
       cluster_sync();  // a CTA's shared memory stays until every other has read it
@@ -824,7 +876,7 @@ struct DeviceFit {
   bool set = false;
   int clusters[kMaxSplit + 1] = {};
 };
-template <bool PAIR, int DC, bool QUART>
+template <int MODE, int DC>
 const DeviceFit* device_fit(int dev) {
   static std::mutex mu;
   static DeviceFit fits[64];
@@ -832,10 +884,10 @@ const DeviceFit* device_fit(int dev) {
   std::lock_guard<std::mutex> lock(mu);
   DeviceFit& f = fits[dev];
   if (!f.set) {
-    const auto kern = k_attn<PAIR, DC, QUART>;
+    const auto kern = k_attn<MODE, DC>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Geo<DC>::kSmem) != cudaSuccess)
       return nullptr;
-    for (int c = 2; !PAIR && c <= kMaxSplit; ++c) {
+    for (int c = 2; MODE != kPairs && c <= kMaxSplit; ++c) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3((unsigned)(148 * c));
       cfg.blockDim = dim3(kThreads);
@@ -857,16 +909,9 @@ const DeviceFit* device_fit(int dev) {
   return &f;
 }
 
-template <bool PAIR, int DC, bool QUART>
-int launch(const AttnMaps& maps, AttnParams& p, int dev, cudaStream_t stream) {
-  const DeviceFit* fit = device_fit<PAIR, DC, QUART>(dev);
-  if (!fit) return SVDQ_ERR_CUDA;
-  p.splits = 1;
-  // The largest cluster of which one for each item is resident at once, with two key tiles to a CTA.
-  const int ktiles = (p.sk + kKeys - 1) / kKeys;
-  for (int c = 2; !PAIR && c <= kMaxSplit && 2 * c <= ktiles; ++c)
-    if (p.items <= fit->clusters[c]) p.splits = c;
-  const int grid = PAIR ? p.step : p.items * p.splits;
+template <int MODE, int DC>
+int launch(const AttnMaps& maps, const AttnParams& p, cudaStream_t stream) {
+  const int grid = MODE == kPairs ? p.step : p.items * p.splits;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
@@ -881,7 +926,59 @@ int launch(const AttnMaps& maps, AttnParams& p, int dev, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.splits > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_attn<PAIR, DC, QUART>, maps, p) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k_attn<MODE, DC>, maps, p) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+}
+
+template <int DC>
+const DeviceFit* device_fit(int mode, int dev) {
+  return mode == kPairs        ? device_fit<kPairs, DC>(dev)
+         : mode == kSplitPairs ? device_fit<kSplitPairs, DC>(dev)
+         : mode == kSingle     ? device_fit<kSingle, DC>(dev)
+                               : device_fit<kQuarter, DC>(dev);
+}
+template <int DC>
+int launch(int mode, const AttnMaps& maps, const AttnParams& p, cudaStream_t stream) {
+  return mode == kPairs        ? launch<kPairs, DC>(maps, p, stream)
+         : mode == kSplitPairs ? launch<kSplitPairs, DC>(maps, p, stream)
+         : mode == kSingle     ? launch<kSingle, DC>(maps, p, stream)
+                               : launch<kQuarter, DC>(maps, p, stream);
+}
+
+// Mode and cluster size for so many tiles of query rows (over all samples and heads), pairs of them, and key tiles: the
+// least of the modes' times, in tenths of a microsecond, as fitted to measurements with heads of 64 and 128, 24 to 1900
+// tiles and 1 to 36 key tiles.  Measured, heads of 128 (one mode against the next best):
+//   24 heads of 1000 tokens over 1024 keys (96 pairs, 192 tiles): pairs 19, single tiles 35 us
+//   24 heads of 512 over 300 (48, 96): pairs 11, single 13;  over 4608: split pairs 43, single 51, pairs 65
+//   24 heads of 128 over 4608 (24 tiles): single 22, pairs 58
+struct Plan {
+  int mode, splits;
+};
+int plan_of(Plan* plan, bool quart, bool wide, int64_t singles, int64_t pairs, int ktiles, int dev) {
+  auto fit_of = [&](int mode) { return wide ? device_fit<2>(mode, dev) : device_fit<1>(mode, dev); };
+  const int64_t sms = device_sm_count(dev);
+  int64_t best = INT64_MAX;
+  auto consider = [&](int mode, int splits, int64_t cost) {
+    if (cost >= best) return;
+    best = cost;
+    *plan = {mode, splits};
+  };
+  auto fold = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
+  if (!quart) {
+    const DeviceFit* f = fit_of(kSplitPairs);
+    if (!f || !fit_of(kPairs)) return SVDQ_ERR_CUDA;
+    const int tile = singles > pairs ? 17 : (wide ? 15 : 12);  // of keys; a pair's only tile is faster
+    consider(kPairs, 1, 40 + fold(pairs, sms) * (10 + tile * ktiles));
+    for (int c = 2; c <= kMaxSplit && 2 * c <= ktiles; ++c)
+      if (pairs <= f->clusters[c]) consider(kSplitPairs, c, 128 + tile * fold(ktiles, c));
+  }
+  const int mode = quart ? kQuarter : kSingle;
+  const DeviceFit* f = fit_of(mode);
+  if (!f) return SVDQ_ERR_CUDA;
+  const int fixed = wide ? 88 : 65, round = wide ? 23 : 15;  // round: two key tiles, one to a stream
+  consider(mode, 1, fold(singles, sms) * (fixed + round * fold(ktiles, 2)));
+  for (int c = 2; c <= kMaxSplit && 2 * c <= ktiles; ++c)
+    if (singles <= f->clusters[c]) consider(mode, c, fixed + (quart ? 0 : 30) + round * fold(ktiles, 2 * c));
+  return SVDQ_OK;
 }
 
 // Tensor map of a [batch, tokens, heads, dim] view.  A dimension of size one, or one with
@@ -1007,13 +1104,15 @@ extern "C" svdq_status svdq_cross_attn(const svdq_attn_args* a, int32_t* status,
   const int64_t bh = (int64_t)p.batch * p.heads_it;
   const int64_t tiles = ((int64_t)p.sq + p.tok_tile - 1) / p.tok_tile;
   const int64_t pairs = (tiles + 1) / 2;
-  // Pairs of tiles once they fill the SMs; below that single tiles, whose keys are split over the SMs that would
-  // stay idle.
-  const bool pair = !quart && bh * pairs >= sms;
   if (bh * tiles > ((int64_t)1 << 30)) return SVDQ_ERR_INVALID_ARG;
+  const bool wide = p.d > 64;
+  Plan plan{};
+  if (int e = plan_of(&plan, quart, wide, bh * tiles, bh * pairs, (p.sk + kKeys - 1) / kKeys, dev)) return (svdq_status)e;
+  const bool pair = plan.mode == kPairs || plan.mode == kSplitPairs;
+  p.splits = plan.splits;
   p.row_tiles = (int)(pair ? pairs : tiles);
   p.items = (int)(bh * p.row_tiles);
-  p.step = pair && p.items > sms ? sms : p.items;  // PAIR: persistent CTAs; else one item to a cluster
+  p.step = plan.mode == kPairs && p.items > sms ? sms : p.items;  // kPairs: persistent CTAs; else one item to a cluster
   p.step_rt = p.step % p.row_tiles;
   p.step_h = p.step / p.row_tiles % p.heads_it;
   p.step_b = p.step / p.row_tiles / p.heads_it;
@@ -1024,7 +1123,7 @@ extern "C" svdq_status svdq_cross_attn(const svdq_attn_args* a, int32_t* status,
                        (uint32_t)p.tok_tile, &p.q_bm, &p.q_hm);
   const int64_t kt = a->kv_tokens > 0 ? a->kv_tokens : 1;
   int st_k = heads_map(&maps.k, kh, a->batch, kt, a->kv_heads, a->dim, 1, kKeys, &p.k_bm, &p.k_hm);
-  if (pair && 32 % p.group == 0) {
+  if (plan.mode == kPairs && 32 % p.group == 0) {
     int bm = 0, hm = 0;
     p.o_tma = 1;
     if (heads_map(&maps.o, a->o, a->batch, a->q_tokens, a->heads, a->dim, (uint32_t)p.group, (uint32_t)(32 / p.group), &bm,
@@ -1036,10 +1135,5 @@ extern "C" svdq_status svdq_cross_attn(const svdq_attn_args* a, int32_t* status,
 
   NvtxRange range("svdq/cross_attn");
   const cudaStream_t s = (cudaStream_t)stream;
-  const bool wide = p.d > 64;
-  if (pair)
-    return (svdq_status)(wide ? launch<true, 2, false>(maps, p, dev, s) : launch<true, 1, false>(maps, p, dev, s));
-  if (quart)
-    return (svdq_status)(wide ? launch<false, 2, true>(maps, p, dev, s) : launch<false, 1, true>(maps, p, dev, s));
-  return (svdq_status)(wide ? launch<false, 2, false>(maps, p, dev, s) : launch<false, 1, false>(maps, p, dev, s));
+  return (svdq_status)(wide ? launch<2>(plan.mode, maps, p, s) : launch<1>(plan.mode, maps, p, s));
 }

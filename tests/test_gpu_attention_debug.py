@@ -37,7 +37,7 @@ for d, rot in ((8, 8), (40, 24), (64, 64), (128, 128), (136, 64), (256, 256)):
         out[f"norm_{d}_{pairs}_q"], out[f"norm_{d}_{pairs}_k"] = bits(q), bits(k)
 for b, sq, sk, hq, hk, d in ((2, 1, 300, 6, 2, 64), (1, 3, 1030, 4, 2, 128), (2, 100, 700, 2, 1, 72),
                              (2, 300, 129, 3, 3, 40), (3, 700, 300, 24, 24, 64), (2, 900, 300, 24, 8, 72),
-                             (2, 900, 300, 40, 20, 128), (1, 2100, 77, 24, 6, 120), (2, 2000, 77, 40, 1, 64)):
+                             (2, 900, 300, 40, 20, 128), (2, 500, 3000, 12, 4, 128), (1, 2100, 77, 24, 6, 120), (2, 2000, 77, 40, 1, 64)):
     q, kv = ac.bf16(g, b, sq, hq, d), ac.bf16(g, b, sk, 2, hk, d)
     mask = (torch.rand(b, sk, generator=g, device="cuda") < 0.8)
     lens = torch.randint(1, sk + 1, (b,), generator=g, device="cuda", dtype=torch.int32)

@@ -71,6 +71,25 @@ def test_query_counts_many_rows(sq):
     _run(5, sq, 200, 32, 32, 64)
 
 
+@pytest.mark.parametrize("b,sq,sk,hq,hk,d", [(1, 500, 4600, 24, 24, 128), (2, 300, 4100, 9, 3, 72), (1, 257, 1500, 12, 12, 128),
+                                             (1, 200, 9000, 4, 2, 64), (1, 1000, 2050, 16, 16, 128)])
+def test_pairs_over_split_keys(b, sq, sk, hq, hk, d):
+    """Too few pairs of tiles for the SMs and many keys: the keys go over a cluster; some of its CTAs have none."""
+    import torch
+
+    _run(b, sq, sk, hq, hk, d)
+    g = ac.generator(24)
+    mask = torch.rand(b, sk, generator=g, device="cuda") < 0.6
+    mask[:, 128:1000] = False
+    _run(b, sq, sk, hq, hk, d, kv_mask=mask)
+    for n in (0, 1, 129, sk // 2):
+        kv_len = torch.full((b,), n, dtype=torch.int32, device="cuda")
+        kv_len[0] = min(n, 200)
+        o = _run(b, sq, sk, hq, hk, d, kv_len=kv_len)[3]
+        if n == 0:
+            assert not o.any()
+
+
 def test_long_keys_split():
     _run(1, 1, 40000, 8, 1, 64)
     _run(2, 2, 20001, 2, 2, 128)
