@@ -5,12 +5,19 @@
 //
 // The floor 2^-100 keeps s and 1/s normal numbers, so a block of zeros (or of subnormals) needs no branch.
 // Two kernels per forward:
-//   k_fp8_quantize: 16 lanes to a block of 128, the maximum by shuffles; bound by memory (2 + 1 bytes an element).
-//   k_gemm_fp8: tcgen05.mma kind::f8f6f4 over one block of 128 inputs at a time into a tensor-memory accumulator
-//     of its own; the scales differ from block to block, so eight warps fold each finished block into sums in
-//     registers, acc += (s_x s_w) d, while the tensor cores work on the next blocks.  The weight scale is one
-//     number for a warp's columns (a tile's column half lies inside one block of 128 rows of W) and the
-//     activation scale one number for a thread's row, so a fold is one fused multiply-add an element.
+//   k_fp8_quantize  16 lanes to a block of 128, the maximum by shuffles; bound by memory (2 + 1 bytes an element:
+//                   4608 x 3072 9.9 us, 4.3 TB/s; 4608 x 12288 36 us, 4.7 TB/s).
+//   the product     tcgen05.mma kind::f8f6f4 over one block of 128 inputs at a time into a tensor-memory accumulator of its
+//                   own; the scales differ from block to block, so warps fold each finished block into sums in registers,
+//                   acc += (s_x s_w) d, while the tensor cores work on the next.  The weight scale is one number for a
+//                   warp's columns (they lie inside one block of 128 rows of W) and the activation scale one number for a
+//                   thread's row, so a fold is one fused multiply-add an element.
+//     k_gemm_fp8      tiles of 128 tokens by 256, 128 or 64 outputs, persistent; or, with fewer tiles than SMs and many
+//                     inputs, a tile to a cluster whose CTAs split the inputs.  4608 x 3072 x 12288: 166 us (2.1 PFLOP/s);
+//                     bound by the fold, which shares tensor memory with the products: a block takes about 800 clocks
+//                     against 512 of products.  Loading 64 columns at a time is what made it fast (32 at a time, the next
+//                     under way meanwhile: 177 us; accumulators freed by halves: 174).
+//     k_gemm_fp8_few  up to 64 tokens: bound by the weight (2 x 3072 x 18432: 13.1 us with the quantizer, 4.3 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -142,17 +149,23 @@ struct Tile {
   static constexpr int kFoldCols = BN / 2;
   static constexpr int kOutCols = kFoldCols < 64 ? kFoldCols : 64;  // columns that go out together
   static constexpr int kOut = 32 * kOutCols * 2;                   // their bytes for the 32 rows of a warp
+  static constexpr int kPartLd = BN + 4;                           // floats between the rows of partial sums
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kFoldWarps * kOut + 512;
   static_assert(kSmem <= 227 * 1024, "shared memory budget");
+  static_assert(128 * kPartLd * 4 <= kStages * kStage, "partial sums fit the stages");
 };
 constexpr int kGemmThreads = 384;
+constexpr int kMaxSplit = 8;  // CTAs of a cluster
+// Of a tile's outputs, four columns each, those that one CTA of a cluster joins: neighbours, in whole lines of 128 bytes
+// (taken in turn instead, a warp's loads from the others' shared memory lie c times as far apart, and cost about that).
+__device__ __forceinline__ int join_share(int units, int splits) { return ((units + splits - 1) / splits + 7) & ~7; }
 // A block of 384 threads starts with 168 registers a thread.  At 256 columns a folding thread holds 128 sums and 64
 // columns on their way, so the folding warps take 224 and leave the others 56: 128 * (2 * 224 + 56) = 384 * 168.
 constexpr int kFoldRegs = 224, kOtherRegs = 56;
 static_assert(128 * (2 * kFoldRegs + kOtherRegs) <= 384 * 168, "the split stays within the launch's registers");
 
 struct F8Params {
-  int M, N, KB, NB, m_tiles, num_tiles, splits;
+  int M, N, KB, NB, m_tiles, num_tiles, splits, per;  // per: blocks of 128 inputs of a CTA
   const float* sx;  // [M, ld]
   const float* sw;  // [NB, ld]
   int ld;
@@ -298,7 +311,7 @@ __device__ __forceinline__ void fold64(uint32_t t, float s, float* a) {
       : "memory");
 }
 
-template <int BN>
+template <int BN, bool SPLIT>
 __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_constant__ F8Maps maps,
                                                              const __grid_constant__ F8Params p) {
   using T = Tile<BN>;
@@ -315,6 +328,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   const int warp = warp_index(), lane = threadIdx.x & 31;
   WaitCtl wc{abort_flag, p.status, p.limit};
+  // SPLIT: a tile to a cluster, whose CTAs take `per` blocks of 128 inputs each (a multiple of 4).
+  const int rank = SPLIT ? (int)cluster_ctarank() : 0;
+  const int tile0 = SPLIT ? (int)blockIdx.x / p.splits : (int)blockIdx.x, step = SPLIT ? p.num_tiles : (int)gridDim.x;
+  const int j_first = SPLIT ? rank * p.per : 0, KB = SPLIT ? min(p.per, p.KB - j_first) : p.KB;
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -348,9 +365,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
       prefetch_tmap(&maps.b);
       int it = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < p.num_tiles && ok; tile += gridDim.x) {
+      for (int tile = tile0; tile < p.num_tiles && ok; tile += step) {
         const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
-        for (int j = 0; j < p.KB; ++j, ++it) {
+        for (int j = 0; j < KB; ++j, ++it) {
           const int s = it % T::kStages;
           if (!timed_wait(&empty[s], ((it / T::kStages) & 1) ^ 1, wc)) {
             ok = false;
@@ -358,8 +375,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
           }
           uint8_t* st = stages + s * T::kStage;
           mbar_arrive_expect_tx(&full[s], T::kStage);
-          tma_load_2d(&maps.a, &full[s], st, j * kBlk, mt * 128);
-          tma_load_2d(&maps.b, &full[s], st + T::kStageA, j * kBlk, nt * BN);
+          tma_load_2d(&maps.a, &full[s], st, (j_first + j) * kBlk, mt * 128);
+          tma_load_2d(&maps.b, &full[s], st + T::kStageA, (j_first + j) * kBlk, nt * BN);
         }
       }
       // No block leaves with copies in flight, whoever gave up on them.
@@ -374,8 +391,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
         int s = 0, b = 0;
         uint32_t s_par = 0, b_par = 1;
         bool ok = true;
-        for (int tile = blockIdx.x; tile < p.num_tiles && ok; tile += gridDim.x) {
-          for (int j = 0; j < p.KB; ++j) {
+        for (int tile = tile0; tile < p.num_tiles && ok; tile += step) {
+          for (int j = 0; j < KB; ++j) {
             ok = timed_wait(&acc_empty[b], b_par, wc) && timed_wait(&full[s], s_par, wc);
             if (!ok) break;
             tc_fence_after();
@@ -411,8 +428,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
     auto scales_of = [&](int mt, int nt) {
       const int m = min(mt * 128 + 32 * q + lane, p.M - 1);  // rows past the last are not stored
       const int nb = min((nt * BN + FC * h) / kBlk, p.NB - 1);  // nor are columns past N
-      px = (const float4*)(p.sx + (long long)m * p.ld);
-      pw = (const float4*)(p.sw + (long long)nb * p.ld);
+      px = (const float4*)(p.sx + (long long)m * p.ld + j_first);
+      pw = (const float4*)(p.sw + (long long)nb * p.ld + j_first);
     };
     auto fetch = [&](float4& x, float4& w) {
       if (SVDQ_INB(p.status, (const char*)px - (const char*)p.sx, 16, 4ll * p.M * p.ld)) x = __ldg(px);
@@ -420,14 +437,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
       ++px;
       ++pw;
     };
-    int mt = blockIdx.x % p.m_tiles, nt = blockIdx.x / p.m_tiles, mt_next = 0, nt_next = 0;
+    int mt = tile0 % p.m_tiles, nt = tile0 / p.m_tiles, mt_next = 0, nt_next = 0;
     scales_of(mt, nt);
     int b = 0;
     uint32_t b_par = 0;
     bool ok = true;
     float4 xn = make_float4(0.f, 0.f, 0.f, 0.f), wn = xn;  // the next four blocks' scales, asked for four folds ahead
     fetch(xn, wn);
-    for (int tile = blockIdx.x; tile < p.num_tiles && ok; tile += gridDim.x) {
+    for (int tile = tile0; tile < p.num_tiles && ok; tile += step) {
       const int m0 = mt * 128 + 32 * q;
       const int n0 = nt * BN + FC * h;
       // The bias is added at the end; bring it near now.
@@ -436,10 +453,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
       float acc[FC];
 #pragma unroll
       for (int i = 0; i < FC; ++i) acc[i] = 0.f;
-      for (int j0 = 0; j0 < p.KB; j0 += 4) {
+      for (int j0 = 0; j0 < KB; j0 += 4) {
         const float sc[4] = {xn.x * wn.x, xn.y * wn.y, xn.z * wn.z, xn.w * wn.w};
-        if (j0 + 4 >= p.KB) {  // the next tile's (past the last tile: any place inside)
-          const int next = min(tile + (int)gridDim.x, p.num_tiles - 1);
+        if (j0 + 4 >= KB) {  // the next tile's (past the last tile: any place inside)
+          const int next = min(tile + step, p.num_tiles - 1);
           mt_next = next % p.m_tiles;
           nt_next = next / p.m_tiles;
           scales_of(mt_next, nt_next);
@@ -447,7 +464,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
         fetch(xn, wn);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          if (j0 + u >= p.KB) break;
+          if (j0 + u >= KB) break;
           ok = timed_wait(&acc_full[b], b_par, wc) && ok;
           __syncwarp();
           tc_fence_after();
@@ -472,6 +489,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
         if (!ok) break;
       }
       if (!ok) break;
+      if constexpr (SPLIT) {  // every load and product of this CTA is complete: the sums go where the stages were
+        float* part = (float*)stages + (32 * q + lane) * T::kPartLd + FC * h;
+#pragma unroll
+        for (int i = 0; i < FC; i += 4) *(float4*)(part + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        break;
+      }
       // A thread has a row, and rows lie far apart in memory: OC columns of the warp's 32 rows go through shared memory
       // (16-byte pieces, swizzled by the row).  64 columns leave by a bulk tensor store, which the next tile's folds need
       // not wait for; 32 columns by neighbouring lanes that write a row's neighbouring pieces.
@@ -522,7 +545,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
       mt = mt_next;
       nt = nt_next;
     }
-    if (OC == 64 && lane == 0) bulk_wait<0>();
+    if (!SPLIT && OC == 64 && lane == 0) bulk_wait<0>();
   }
 
   tc_fence_before();
@@ -530,6 +553,53 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
   if (warp == T::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, T::kCols);
+  }
+  if constexpr (SPLIT) {  // join: four columns of a row to a thread, U of them at once
+    constexpr int U = 4;
+    const int m0 = tile0 % p.m_tiles * 128, n0 = tile0 / p.m_tiles * BN;
+    const int units = min(128, p.M - m0) * (BN / 4), share = join_share(units, p.splits);
+    const int first = rank * share, total = min(share, units - first);  // this CTA's (none, if negative)
+    cluster_sync();
+    if (*abort_flag == 0) {
+      const uint32_t base = smem_u32(stages);
+      for (int u0 = threadIdx.x; u0 < total; u0 += U * kGemmThreads) {
+        int row[U], n[U];
+        uint32_t from[U];
+        float4 y[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          const int u = first + min(u0 + j * kGemmThreads, total - 1);
+          const int c = 4 * (u % (BN / 4));
+          row[j] = u / (BN / 4);
+          n[j] = n0 + c;
+          from[j] = base + (uint32_t)(row[j] * T::kPartLd + c) * 4;
+          y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (n[j] < p.N && SVDQ_INB(p.status, 4ll * n[j], 16, 4ll * p.N)) y[j] = __ldg((const float4*)(p.bias + n[j]));
+        }
+#pragma unroll 2
+        for (int r = 0; r < p.splits; ++r) {
+          float4 x[U];
+#pragma unroll
+          for (int j = 0; j < U; ++j) x[j] = dsmem_ld_f32x4(dsmem_addr(from[j], r));
+#pragma unroll
+          for (int j = 0; j < U; ++j) {
+            y[j].x += x[j].x;
+            y[j].y += x[j].y;
+            y[j].z += x[j].z;
+            y[j].w += x[j].w;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          const long long at = (long long)(m0 + row[j]) * p.N + n[j];
+          if (u0 + j * kGemmThreads < total && n[j] < p.N && SVDQ_INB(p.status, 2 * at, 8, 2ll * p.M * p.N)) {
+            __nv_bfloat162 lo = __floats2bfloat162_rn(y[j].x, y[j].y), hi = __floats2bfloat162_rn(y[j].z, y[j].w);
+            *(uint2*)(p.Y + at) = make_uint2(*(uint32_t*)&lo, *(uint32_t*)&hi);
+          }
+        }
+      }
+    }
+    cluster_sync();  // a CTA's shared memory stays until every other has read it
   }
 }
 
@@ -539,7 +609,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
 // holds a row's sums for all tokens.  A cluster's CTAs split the inputs where there are fewer tiles than SMs, and join
 // through distributed shared memory in the order of their ranks.  Two CTAs share an SM.  The loads of W do not wait for
 // the quantizer.
-constexpr int kMaxSplit = 8;
 template <int BT>
 struct Few {
   static constexpr int kStageW = 128 * kBlk, kStage = kStageW + BT * kBlk;
@@ -710,7 +779,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_gemm_fp8_few(const __grid_co
   cluster_sync();
   if (good) {
     const uint32_t base = smem_u32(part);
-    for (int u = threadIdx.x * p.splits + rank; u < p.M * 32; u += kFewThreads * p.splits) {
+    const int share = join_share(p.M * 32, p.splits), end = min(p.M * 32, (rank + 1) * share);
+    for (int u = rank * share + threadIdx.x; u < end; u += kFewThreads) {
       const int t = u >> 5, c = 4 * (u & 31), n = nt * 128 + c;
       float4 x[kMaxSplit];
 #pragma unroll
@@ -748,95 +818,124 @@ int launch_f8_quantize(const svdq_fp8_layer* L, const void* X, int64_t M, uint8_
              : SVDQ_ERR_CUDA;
 }
 
-template <int BN>
-int launch_f8_tile(const svdq_fp8_layer* L, const F8Maps& maps, F8Params& p, cudaStream_t stream) {
-  using T = Tile<BN>;
-  {  // the shared-memory attribute belongs to the kernel on each device: set it once per device
-    static std::mutex mu;
-    static bool attr_set[64] = {};
-    if (L->device < 0 || L->device >= 64) return SVDQ_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!attr_set[L->device]) {
-      if (cudaFuncSetAttribute(k_gemm_fp8<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)T::kSmem) !=
-          cudaSuccess)
-        return SVDQ_ERR_CUDA;
-      attr_set[L->device] = true;
-    }
-  }
-  p.m_tiles = (p.M + 127) / 128;
-  p.num_tiles = p.m_tiles * ((p.N + BN - 1) / BN);
-  const int sms = device_sm_count(L->device);
-  const int grid = p.num_tiles < sms ? p.num_tiles : sms;
-  return launch_pdl(k_gemm_fp8<BN>, dim3((unsigned)grid), dim3(kGemmThreads), T::kSmem, stream, maps, p) == cudaSuccess
-             ? SVDQ_OK
-             : SVDQ_ERR_CUDA;
-}
-
-// Once per device: the shared-memory attribute, and how many clusters of each size are resident at once.
-struct FewFit {
+// Once per device and kernel: the shared-memory attribute, and how many clusters of each size are resident at once.
+struct Fit {
   bool set = false;
   int clusters[kMaxSplit + 1] = {};
 };
-template <int BT>
-int launch_f8_few(const svdq_fp8_layer* L, const F8Maps& maps, F8Params& p, cudaStream_t stream) {
-  using T = Few<BT>;
-  static std::mutex mu;
-  static FewFit fits[64];
-  if (L->device < 0 || L->device >= 64) return SVDQ_ERR_CUDA;
+cudaLaunchConfig_t cluster_config(int grid, int threads, size_t smem, int splits, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kFewThreads);
-  cfg.dynamicSmemBytes = T::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.x = (unsigned)splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  const int tiles = p.NB;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    FewFit& f = fits[L->device];
-    if (!f.set) {
-      if (cudaFuncSetAttribute(k_gemm_fp8_few<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)T::kSmem) !=
-          cudaSuccess)
-        return SVDQ_ERR_CUDA;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+template <auto kernel>
+const Fit* fit_of(int dev, int threads, size_t smem, bool clusters) {
+  static std::mutex mu;
+  static Fit fits[64];
+  if (dev < 0 || dev >= 64) return nullptr;
+  std::lock_guard<std::mutex> lock(mu);
+  Fit& f = fits[dev];
+  if (!f.set) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return nullptr;
+    for (int c = 2; clusters && c <= kMaxSplit; ++c) {
+      cudaLaunchAttribute attr[2];
+      cudaLaunchConfig_t cfg = cluster_config(296 * c, threads, smem, c, attr);
       cfg.numAttrs = 1;
-      for (int c = 2; c <= kMaxSplit; ++c) {
-        attr[0].val.clusterDim.x = (unsigned)c;
-        cfg.gridDim = dim3((unsigned)(296 * c));
-        if (cudaOccupancyMaxActiveClusters(&f.clusters[c], k_gemm_fp8_few<BT>, &cfg) != cudaSuccess) {
-          cudaGetLastError();
-          f.clusters[c] = 0;
-        }
+      if (cudaOccupancyMaxActiveClusters(&f.clusters[c], kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        f.clusters[c] = 0;
       }
-      f.set = true;
     }
-    // The largest cluster of which one for each tile is resident at once, two blocks of 128 to a CTA at least.
-    p.splits = 1;
-    for (int c = 2; c <= kMaxSplit && 2 * c <= p.KB; ++c)
-      if (tiles <= f.clusters[c]) p.splits = c;
+    f.set = true;
   }
+  return &f;
+}
+template <int BN, bool SPLIT>
+const Fit* tile_fit(int dev) {
+  return fit_of<k_gemm_fp8<BN, SPLIT>>(dev, kGemmThreads, Tile<BN>::kSmem, SPLIT);
+}
+template <int BN, bool SPLIT>
+int launch_f8_tile(const F8Maps& maps, const F8Params& p, int grid, cudaStream_t stream) {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = cluster_config(grid, kGemmThreads, Tile<BN>::kSmem, p.splits, attr);
+  if (!SPLIT) {
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;
+  }
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, k_gemm_fp8<BN, SPLIT>, maps, p) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+}
+
+template <int BT>
+int launch_f8_few(const svdq_fp8_layer* L, const F8Maps& maps, F8Params& p, cudaStream_t stream) {
+  using T = Few<BT>;
+  const Fit* f = fit_of<k_gemm_fp8_few<BT>>(L->device, kFewThreads, T::kSmem, true);
+  if (!f) return SVDQ_ERR_CUDA;
+  const int tiles = p.NB;
+  // The largest cluster of which one for each tile is resident at once, two blocks of 128 to a CTA at least; up to four
+  // blocks are faster than a join (2 tokens, 512 -> 1024: 4.0 us, two CTAs 4.6;  1024 -> 1024: four 4.6, two 5.3).
+  p.splits = 1;
+  for (int c = 2; c <= kMaxSplit && 2 * c <= p.KB && p.KB > 4; ++c)
+    if (tiles <= f->clusters[c]) p.splits = c;
   while ((p.KB + p.splits - 1) / p.splits > T::kMaxBlocks) {
     if (p.splits == kMaxSplit) return -1;  // more inputs than the table of scales holds: the tiles above take them
     ++p.splits;
   }
-  cfg.gridDim = dim3((unsigned)(tiles * p.splits));
-  attr[0].val.clusterDim.x = (unsigned)p.splits;
-  cfg.numAttrs = 2;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = cluster_config(tiles * p.splits, kFewThreads, T::kSmem, p.splits, attr);
+  cfg.stream = stream;
   return cudaLaunchKernelEx(&cfg, k_gemm_fp8_few<BT>, maps, p) == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
+}
+
+// Tile width and cluster size: the least estimate of the time, in nanoseconds beyond the launch, as fitted to measurements
+// with 30 to 2048 tokens, 320 to 9216 outputs and 512 to 9728 inputs of every width and cluster size.  Measured, us:
+//   128 tokens, 9728 -> 1024: 64 columns over clusters of 5 11.9, of 2 16.5, unsplit 24.4; 128 columns over 7 13.5
+//   512 tokens, 9728 -> 1024: 128 columns over 4 17.1; 64 over 2 19.2; unsplit 27.1
+//   512 tokens, 3072 -> 3072: 128 columns 12.9; 256 16.8; 64 17.9 (two rounds over the SMs)
+//   1024 tokens, 3072 -> 9216: 256 columns 30.6; 128 36.5; 64 58.7
+struct F8Plan {
+  int width, splits, per;  // width: 0, 1, 2 for 256, 128, 64 columns
+};
+int f8_plan(F8Plan* plan, int64_t M, int64_t N, int64_t KB, int dev) {
+  const Fit* fits[3] = {tile_fit<256, false>(dev), tile_fit<128, true>(dev), tile_fit<64, true>(dev)};
+  if (!fits[0] || !fits[1] || !fits[2] || !tile_fit<128, false>(dev) || !tile_fit<64, false>(dev)) return SVDQ_ERR_CUDA;
+  const int64_t sms = device_sm_count(dev), rows = std::min<int64_t>(M, 128);
+  static const int kBlock[3] = {480, 290, 250}, kTile[3] = {700, 500, 500};       // a block of 128 inputs, a tile
+  static const int kJoin[3] = {0, 400, 0}, kJoinCta[3] = {0, 400, 250};           // of 128 rows: once, and for each CTA
+  int64_t best = INT64_MAX;
+  for (int w = 0; w < 3; ++w) {
+    const int64_t tiles = (M + 127) / 128 * ((N + (256 >> w) - 1) / (256 >> w));
+    for (int c = 1; c <= (w ? kMaxSplit : 1); ++c) {
+      const int64_t per = c == 1 ? KB : (KB + 4 * c - 1) / (4 * c) * 4;  // scales are read four blocks at a time
+      // (as many clusters as fit at once took a second round on some devices)
+      if (c > 1 && (tiles >= fits[w]->clusters[c] || (KB + per - 1) / per != c)) continue;
+      const int64_t rounds = c > 1 ? 1 : (tiles + sms - 1) / sms;
+      const int64_t cost =
+          rounds * (per * kBlock[w] + kTile[w]) + (c > 1 ? 1500 + (kJoin[w] + c * kJoinCta[w]) * rows / 128 : 0);
+      if (cost < best) {
+        best = cost;
+        *plan = {w, c, (int)per};
+      }
+    }
+  }
+  return SVDQ_OK;
 }
 
 int launch_f8_gemm(const svdq_fp8_layer* L, int64_t M, void* Y, uint8_t* ws, cudaStream_t stream) {
   const F8Ws w = f8_ws_layout(M, L->K);
   F8Maps maps;
   std::memset(&maps, 0, sizeof(maps));
-  const int few = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 0));
-  int st = encode_tmap_2d(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, ws + w.codes, (uint64_t)L->K, (uint64_t)M,
-                          (uint64_t)L->K, kBlk, few ? (uint32_t)few : 128, CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st != SVDQ_OK) return st;
   F8Params p{};
   p.M = (int)M;
   p.N = (int)L->N;
@@ -849,6 +948,14 @@ int launch_f8_gemm(const svdq_fp8_layer* L, int64_t M, void* Y, uint8_t* ws, cud
   p.Y = (uint16_t*)Y;
   p.status = (int*)(ws + w.status);
   p.limit = wait_limit_cycles();
+  // From 33 tokens only while clusters of four and more fit beside one another, and for 9 to 64 blocks of 128 inputs:
+  // 60 tokens, 3072 -> 3072 7.9 us against 9.0 with the tiles below, but 3072 -> 9216 11.4 against 10.0, 512 -> 3072 6.9
+  // against 5.4 and 12288 -> 600 11.2 against 10.1.  (30 tokens, 3072 -> 9216: 8.9 against 12.2.)
+  const bool narrow = 4 * ((L->N + kBlk - 1) / kBlk) <= device_sm_count(L->device) && p.KB > 8 && p.KB <= 64;
+  const int few = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 && narrow ? 64 : 0));
+  int st = encode_tmap_2d(&maps.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, ws + w.codes, (uint64_t)L->K, (uint64_t)M,
+                          (uint64_t)L->K, kBlk, few ? (uint32_t)few : 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != SVDQ_OK) return st;
   if (few) {
     maps.b = L->map_w[1];
     st = few == 16   ? launch_f8_few<16>(L, maps, p, stream)
@@ -859,19 +966,26 @@ int launch_f8_gemm(const svdq_fp8_layer* L, int64_t M, void* Y, uint8_t* ws, cud
                         (uint64_t)L->K, kBlk, 128, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != SVDQ_OK) return st;
   }
-  // Rounds of tiles over the SMs times the time of a tile's block: the widest tiles where they fill the SMs, narrower
-  // ones where there are too few (a tile's fixed part counts as about 64 columns).
-  const int64_t sms = device_sm_count(L->device);
-  auto cost = [&](int64_t bn) {
-    return ((M + 127) / 128 * ((L->N + bn - 1) / bn) + sms - 1) / sms * (bn + 64);
-  };
-  const int best = cost(256) <= cost(128) && cost(256) <= cost(64) ? 0 : (cost(128) <= cost(64) ? 1 : 2);
-  maps.b = L->map_w[best];
+  F8Plan plan{};
+  st = f8_plan(&plan, M, L->N, p.KB, L->device);
+  if (st != SVDQ_OK) return st;
+  p.splits = plan.splits;
+  p.per = plan.per;
+  p.m_tiles = (p.M + 127) / 128;
+  p.num_tiles = p.m_tiles * (int)((L->N + (256 >> plan.width) - 1) / (256 >> plan.width));
+  maps.b = L->map_w[plan.width];
+  if (plan.splits > 1) {
+    const int grid = p.num_tiles * plan.splits;
+    return plan.width == 1 ? launch_f8_tile<128, true>(maps, p, grid, stream)
+                           : launch_f8_tile<64, true>(maps, p, grid, stream);
+  }
   st = encode_tmap_2d(&maps.y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, (uint64_t)L->N, (uint64_t)M, (uint64_t)L->N * 2, 64, 32,
                       CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != SVDQ_OK) return st;
-  return best == 0 ? launch_f8_tile<256>(L, maps, p, stream)
-                   : best == 1 ? launch_f8_tile<128>(L, maps, p, stream) : launch_f8_tile<64>(L, maps, p, stream);
+  const int sms = device_sm_count(L->device), grid = p.num_tiles < sms ? p.num_tiles : sms;
+  return plan.width == 0   ? launch_f8_tile<256, false>(maps, p, grid, stream)
+         : plan.width == 1 ? launch_f8_tile<128, false>(maps, p, grid, stream)
+                           : launch_f8_tile<64, false>(maps, p, grid, stream);
 }
 
 }  // namespace

@@ -79,6 +79,17 @@ def test_parity(M, K, N):
     print(M, K, N, _check(lin, x, lin.forward(x), qw, sw, b))
 
 
+@pytest.mark.parametrize("M", [1, 16, 31, 33, 64, 65, 128, 130, 300, 700])
+@pytest.mark.parametrize("K,N", [(144, 72), (528, 328), (1040, 1000), (1552, 136), (2064, 3080), (4112, 520), (9744, 264)])
+def test_every_split(M, K, N):
+    """Tokens, inputs and outputs for which the inputs go over clusters of every size, tiles of every width."""
+    lin, qw, sw, b = _layer(K, N, K + N)
+    x = _x(ac.generator(M), M, K)
+    y = lin.forward(x)
+    _check(lin, x, y, qw, sw, b)
+    assert (lin.forward(x) == y).all()
+
+
 @pytest.mark.parametrize("K,N", [(3072, 12288), (12288, 3072)])
 def test_mlp_shapes(K, N):
     lin, qw, sw, b = _layer(K, N, K)
