@@ -45,6 +45,11 @@ __device__ __forceinline__ void unpack(const uint4& u, float (&f)[8]) {
   }
 }
 
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *(const uint32_t*)&v;
+}
+
 // One token of one side.  PAIRS: 0 adjacent, 1 halves.  The weight is multiplied into the cosines and sines once, so
 // that an output costs a product with 1/rms, a product and a fused multiply-add (two outputs to an instruction for
 // adjacent pairs); the kernel issues about as long as it moves data, so instructions count.
@@ -57,29 +62,50 @@ __device__ __forceinline__ Place place_of(const Side& sd, long long token) {
   const unsigned t = (unsigned)token, n = (unsigned)sd.tokens;  // batch * tokens <= 2^30
   return {(int)(t / n), (int)(t % n)};
 }
-template <int LG>
+// The first elements of a lane's two groups of four: adjacent pairs, eight neighbours; halves, four elements and their four
+// partners rot/2 further on, and past rot eight neighbours again, so that no lane needs another's elements.
+struct Groups {
+  int a, b;
+  bool turned;  // rotated (adjacent pairs: the first group; a row's rotated part may end between the two)
+};
+template <int LG, int PAIRS>
+__device__ __forceinline__ Groups groups_of(const NormParams& p, const Side& sd) {
+  const int sub = threadIdx.x % LG, rot = sd.rope ? p.rot : 0;
+  if (PAIRS == 1 && 8 * sub < rot) return {4 * sub, 4 * sub + rot / 2, true};
+  return {8 * sub, 8 * sub + 4, 8 * sub < rot};
+}
+template <int LG, int PAIRS>
 __device__ __forceinline__ void load_heads(const NormParams& p, const Side& sd, const Place& at, int h0,
                                            uint4 (&u)[kUnroll]) {
   constexpr int ROWS = kThreads / LG;
-  const int e0 = 8 * (threadIdx.x % LG);
-  const long long xb = at.b * sd.x_sb + at.s * sd.x_st + e0;
+  const Groups e = groups_of<LG, PAIRS>(p, sd);
+  const bool on = 8 * (int)(threadIdx.x % LG) < p.dim;
+  const long long xb = at.b * sd.x_sb + at.s * sd.x_st;
 #pragma unroll
   for (int k = 0; k < kUnroll; ++k) {
     const int h = h0 + k * ROWS + (int)threadIdx.x / LG;
     u[k] = make_uint4(0, 0, 0, 0);
-    const long long off = xb + (long long)h * sd.x_sh;
-    if (e0 < p.dim && h < sd.heads && SVDQ_INB(p.status, 2 * off, 16, sd.x_extent)) u[k] = *(const uint4*)(sd.x + off);
+    if (!on || h >= sd.heads) continue;
+    const long long off = xb + (long long)h * sd.x_sh + e.a;
+    if constexpr (PAIRS == 0) {
+      if (SVDQ_INB(p.status, 2 * off, 16, sd.x_extent)) u[k] = *(const uint4*)(sd.x + off);
+    } else {
+      const long long off_b = off - e.a + e.b;
+      if (SVDQ_INB(p.status, 2 * off, 8, sd.x_extent) && SVDQ_INB(p.status, 2 * off_b, 8, sd.x_extent)) {
+        const uint2 lo = *(const uint2*)(sd.x + off), hi = *(const uint2*)(sd.x + off_b);
+        u[k] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      }
+    }
   }
 }
 template <int LG, int PAIRS>
 __device__ __forceinline__ void do_side(const NormParams& p, const Side& sd, long long token, const Place& place,
                                         uint4 (&u)[kUnroll]) {
   constexpr int ROWS = kThreads / LG, UNROLL = kUnroll;
-  const int sub = threadIdx.x % LG, first = threadIdx.x / LG;
-  const int e0 = 8 * sub;
-  const bool on = e0 < p.dim;
+  const int first = threadIdx.x / LG;
+  const Groups e = groups_of<LG, PAIRS>(p, sd);
+  const bool on = 8 * (int)(threadIdx.x % LG) < p.dim;
   const int b = place.b, s = place.s;
-  const int half = p.rot >> 1;
   const float* r = nullptr;  // the token's row of cosines and sines
   [[maybe_unused]] long long row = s;
   bool bad = false;
@@ -92,68 +118,52 @@ __device__ __forceinline__ void do_side(const NormParams& p, const Side& sd, lon
     r = sd.rope + row * p.rot;
   }
   if (bad && p.status && threadIdx.x == 0) atomicCAS(p.status, 0, SVDQ_ERR_INVALID_ARG);
-  float w[8];
+  float w[8];  // of the first group, of the second
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = 1.f;
-  if (sd.weight && on && SVDQ_INB(p.status, 2 * e0, 16, 2 * p.dim)) unpack(__ldg((const uint4*)(sd.weight + e0)), w);
-  // Coefficients of a lane's eight elements, four (g) at a time; ca multiplies the element, cb its partner.
-  // Adjacent: packed over the group's two pairs, [g][0] for the first of a pair, [g][1] for the second.
+  if (sd.weight && on && SVDQ_INB(p.status, 2 * e.a, 8, 2 * p.dim) && SVDQ_INB(p.status, 2 * e.b, 8, 2 * p.dim)) {
+    const uint2 lo = __ldg((const uint2*)(sd.weight + e.a)), hi = __ldg((const uint2*)(sd.weight + e.b));
+    unpack(make_uint4(lo.x, lo.y, hi.x, hi.y), w);
+  }
+  // Coefficients of a lane's four pairs, two pairs (g) to a register: ca multiplies the element, cb its partner;
+  // [g][0] for the firsts of the pairs, [g][1] for the seconds.
   uint64_t ca2[2][2], cb2[2][2];
-  float ca[8], cb[8];
   bool turned[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const int e = e0 + 4 * g;
-    turned[g] = r != nullptr && e < p.rot;
-    if constexpr (PAIRS == 0) {
-      float4 t = make_float4(1.f, 0.f, 1.f, 0.f);
-      if (turned[g] && SVDQ_INB(p.status, 4 * (row * p.rot + e), 16, 4 * sd.rope_rows * p.rot))
-        t = __ldg((const float4*)(r + e));
-      const float* v = w + 4 * g;
-      ca2[g][0] = pack2(v[0] * t.x, v[2] * t.z);
-      cb2[g][0] = pack2(-v[1] * t.y, -v[3] * t.w);
-      ca2[g][1] = pack2(v[1] * t.x, v[3] * t.z);
-      cb2[g][1] = pack2(v[0] * t.y, v[2] * t.w);
-    } else {
-      float pw[4] = {1.f, 1.f, 1.f, 1.f};  // the partners' weights
-      const int at = e < half ? e : e - half;
-      const int pe = e < half ? e + half : e - half;
-      if (turned[g] && sd.weight && SVDQ_INB(p.status, 2 * pe, 8, 2 * p.dim)) {
-        const uint2 u = __ldg((const uint2*)(sd.weight + pe));
-        pw[0] = __uint_as_float(u.x << 16);
-        pw[1] = __uint_as_float(u.x & 0xFFFF0000u);
-        pw[2] = __uint_as_float(u.y << 16);
-        pw[3] = __uint_as_float(u.y & 0xFFFF0000u);
-      }
-      float4 t0 = make_float4(1.f, 0.f, 1.f, 0.f), t1 = t0;
-      if (turned[g] && SVDQ_INB(p.status, 4 * (row * p.rot + 2 * at), 32, 4 * sd.rope_rows * p.rot)) {
-        t0 = __ldg((const float4*)(r + 2 * at));
-        t1 = __ldg((const float4*)(r + 2 * at) + 1);
-      }
-      const float cs[4] = {t0.x, t0.z, t1.x, t1.z}, sn[4] = {t0.y, t0.w, t1.y, t1.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ca[4 * g + i] = w[4 * g + i] * cs[i];
-        cb[4 * g + i] = (e < half ? -sn[i] : sn[i]) * pw[i];  // the first of a pair subtracts
-      }
-    }
+    // adjacent: pairs 2g, 2g + 1 are the lane's group g; halves: elements 2g, 2g + 1 of the first group, and of the second
+    const int f0 = PAIRS == 0 ? 4 * g : 2 * g, f1 = PAIRS == 0 ? 4 * g + 2 : 2 * g + 1;        // firsts, among w
+    const int s0 = PAIRS == 0 ? 4 * g + 1 : 4 + 2 * g, s1 = PAIRS == 0 ? 4 * g + 3 : 5 + 2 * g;  // seconds
+    turned[g] = PAIRS == 0 ? r != nullptr && e.a + 4 * g < p.rot : e.turned;
+    float4 t = make_float4(1.f, 0.f, 1.f, 0.f);
+    const int at = PAIRS == 0 ? e.a + 4 * g : 2 * e.a + 4 * g;  // in the table's row
+    if (turned[g] && SVDQ_INB(p.status, 4 * (row * p.rot + at), 16, 4 * sd.rope_rows * p.rot))
+      t = __ldg((const float4*)(r + at));
+    ca2[g][0] = pack2(w[f0] * t.x, w[f1] * t.z);
+    cb2[g][0] = pack2(-w[s0] * t.y, -w[s1] * t.w);
+    ca2[g][1] = pack2(w[s0] * t.x, w[s1] * t.z);
+    cb2[g][1] = pack2(w[f0] * t.y, w[f1] * t.w);
   }
   const long long yb = b * sd.y_sb + s * sd.y_st;
   const float inv_dim = 1.f / (float)p.dim;
   // every lane takes every round (the shuffles need whole warps); heads past the last read nothing
   for (int h0 = 0; h0 < sd.heads; h0 += ROWS * UNROLL) {
-    if (h0 > 0) load_heads<LG>(p, sd, place, h0, u);
+    if (h0 > 0) load_heads<LG, PAIRS>(p, sd, place, h0, u);
 #pragma unroll
     for (int k = 0; k < UNROLL; ++k) {
       if (h0 + k * ROWS >= sd.heads) break;
       const int h = h0 + k * ROWS + first;
       const uint32_t in[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-      // lo[g]: first and third element of the group, hi[g]: second and fourth
-      uint64_t lo[2], hi[2], ss2 = 0;
+      uint64_t lo[2], hi[2], ss2 = 0;  // the firsts of the pairs, the seconds
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        lo[g] = pack2(in[2 * g] << 16, in[2 * g + 1] << 16);
-        hi[g] = pack2(in[2 * g] & 0xFFFF0000u, in[2 * g + 1] & 0xFFFF0000u);
+        if constexpr (PAIRS == 0) {
+          lo[g] = pack2(in[2 * g] << 16, in[2 * g + 1] << 16);
+          hi[g] = pack2(in[2 * g] & 0xFFFF0000u, in[2 * g + 1] & 0xFFFF0000u);
+        } else {
+          lo[g] = pack2(in[g] << 16, in[g] & 0xFFFF0000u);
+          hi[g] = pack2(in[2 + g] << 16, in[2 + g] & 0xFFFF0000u);
+        }
         ss2 = fma2(lo[g], lo[g], ss2);
         ss2 = fma2(hi[g], hi[g], ss2);
       }
@@ -164,59 +174,31 @@ __device__ __forceinline__ void do_side(const NormParams& p, const Side& sd, lon
       float inv = rsqrtf(fmaf(ss, inv_dim, p.eps));
       if (bad) inv = __int_as_float(0x7FC00000);
       const uint64_t inv2 = pack2(inv, inv);
-      float2 y[2][2];  // [g][0] of the firsts of the group's pairs, [g][1] of the seconds
+      float2 y[2][2];  // [g][0] of the firsts of two pairs, [g][1] of the seconds
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         lo[g] = mul2(lo[g], inv2);
         hi[g] = mul2(hi[g], inv2);
-        if constexpr (PAIRS == 0) {
-          uint64_t a = mul2(lo[g], ca2[g][0]), c = mul2(hi[g], ca2[g][1]);
-          if (turned[g]) {
-            a = fma2(hi[g], cb2[g][0], a);
-            c = fma2(lo[g], cb2[g][1], c);
-          }
-          y[g][0] = unpack2(a);
-          y[g][1] = unpack2(c);
+        uint64_t a = mul2(lo[g], ca2[g][0]), c = mul2(hi[g], ca2[g][1]);
+        if (turned[g]) {
+          a = fma2(hi[g], cb2[g][0], a);
+          c = fma2(lo[g], cb2[g][1], c);
         }
+        y[g][0] = unpack2(a);
+        y[g][1] = unpack2(c);
       }
-      if constexpr (PAIRS == 1) {
-        float v[8];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const float2 l = unpack2(lo[g]), q = unpack2(hi[g]);
-          v[4 * g] = l.x;
-          v[4 * g + 1] = q.x;
-          v[4 * g + 2] = l.y;
-          v[4 * g + 3] = q.y;
+      const long long off = yb + (long long)h * sd.y_sh + e.a;
+      if (!on || h >= sd.heads) continue;
+      if constexpr (PAIRS == 0) {
+        if (SVDQ_INB(p.status, 2 * off, 16, sd.y_extent))
+          *(uint4*)(sd.y + off) = make_uint4(bf16x2(y[0][0].x, y[0][1].x), bf16x2(y[0][0].y, y[0][1].y),
+                                             bf16x2(y[1][0].x, y[1][1].x), bf16x2(y[1][0].y, y[1][1].y));
+      } else {
+        const long long off_b = off - e.a + e.b;
+        if (SVDQ_INB(p.status, 2 * off, 8, sd.y_extent) && SVDQ_INB(p.status, 2 * off_b, 8, sd.y_extent)) {
+          *(uint2*)(sd.y + off) = make_uint2(bf16x2(y[0][0].x, y[0][0].y), bf16x2(y[1][0].x, y[1][0].y));
+          *(uint2*)(sd.y + off_b) = make_uint2(bf16x2(y[0][1].x, y[0][1].y), bf16x2(y[1][1].x, y[1][1].y));
         }
-        float o[8];
-        // the partner of element e is e +- rot/2; its place among a lane's eight is i or (rot/2 = 4 mod 8) i ^ 4
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int e = e0 + i;
-          const int pe = e < half ? e + half : (e < p.rot ? e - half : e);
-          const float send = (half & 4) ? v[i ^ 4] : v[i];
-          const float partner = __shfl_sync(0xffffffffu, send, pe >> 3, LG);
-          o[i] = v[i] * ca[i];
-          if (turned[i >> 2]) o[i] = fmaf(partner, cb[i], o[i]);
-        }
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          y[g][0] = make_float2(o[4 * g], o[4 * g + 2]);
-          y[g][1] = make_float2(o[4 * g + 1], o[4 * g + 3]);
-        }
-      }
-      const long long off = yb + (long long)h * sd.y_sh + e0;
-      if (on && h < sd.heads && SVDQ_INB(p.status, 2 * off, 16, sd.y_extent)) {
-        uint32_t o[4];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          __nv_bfloat162 h0v = __floats2bfloat162_rn(y[g][0].x, y[g][1].x);
-          __nv_bfloat162 h1v = __floats2bfloat162_rn(y[g][0].y, y[g][1].y);
-          o[2 * g] = *(uint32_t*)&h0v;
-          o[2 * g + 1] = *(uint32_t*)&h1v;
-        }
-        *(uint4*)(sd.y + off) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
@@ -230,8 +212,8 @@ __global__ void __launch_bounds__(kThreads, 6) k_qk_norm_rope(const __grid_const
   for (long long token = blockIdx.x; token < n; token += gridDim.x) {
     uint4 u0[kUnroll], u1[kUnroll];
     const Place at0 = place_of(p.side[0], token), at1 = place_of(p.side[1], token);
-    if (token < n0) load_heads<LG>(p, p.side[0], at0, 0, u0);
-    if (token < n1) load_heads<LG>(p, p.side[1], at1, 0, u1);
+    if (token < n0) load_heads<LG, PAIRS>(p, p.side[0], at0, 0, u0);
+    if (token < n1) load_heads<LG, PAIRS>(p, p.side[1], at1, 0, u1);
     if (token < n0) do_side<LG, PAIRS>(p, p.side[0], token, at0, u0);
     if (token < n1) do_side<LG, PAIRS>(p, p.side[1], token, at1, u1);
   }
