@@ -2,10 +2,11 @@
 //
 //   y = rot( w * x / sqrt(mean x^2 + eps) ),  rot: (a, c) -> (a cos - c sin, a sin + c cos).
 //
-// Bound by memory: every element is read once and written once, 16 bytes (8 elements) to a lane.  A
-// head's row of dim elements lies in LG lanes (the power of two >= dim / 8), so the mean is a sum over
-// shuffles and no shared memory is needed.  A CTA takes one token at a time: its lanes keep the token's
-// cosines and sines and the weight in registers and walk the token's heads with them.
+// Bound by memory: every element is read once and written once, 16 bytes (8 elements) to a lane (9216 tokens of 24 + 24
+// heads of 128: 43.7 us, 5.2 TB/s; half-split pairs, whose elements come in two pieces of 8 bytes, 46.4).  A head's row of
+// dim elements lies in LG lanes (the power of two >= dim / 8), so the mean is a sum over shuffles and no shared memory
+// is needed.  A CTA takes one token at a time: its lanes keep the token's cosines and sines and the weight in registers
+// and walk the token's heads with them.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -15,8 +16,6 @@
 
 namespace svdq {
 namespace {
-
-constexpr int kThreads = 128;
 
 struct Side {
   const uint16_t* x;
@@ -51,8 +50,8 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 }
 
 // One token of one side.  PAIRS: 0 adjacent, 1 halves.  The weight is multiplied into the cosines and sines once, so
-// that an output costs a product with 1/rms, a product and a fused multiply-add (two outputs to an instruction for
-// adjacent pairs); the kernel issues about as long as it moves data, so instructions count.
+// that an output costs a product with 1/rms, a product and a fused multiply-add (two outputs to an instruction); the
+// kernel issues about as long as it moves data, so instructions count.
 // `u` holds the first heads' elements, asked for before anything else of the token.
 constexpr int kUnroll = 3;  // heads of a lane in flight for each side
 struct Place {
@@ -74,10 +73,10 @@ __device__ __forceinline__ Groups groups_of(const NormParams& p, const Side& sd)
   if (PAIRS == 1 && 8 * sub < rot) return {4 * sub, 4 * sub + rot / 2, true};
   return {8 * sub, 8 * sub + 4, 8 * sub < rot};
 }
-template <int LG, int PAIRS>
+template <int T, int LG, int PAIRS>
 __device__ __forceinline__ void load_heads(const NormParams& p, const Side& sd, const Place& at, int h0,
                                            uint4 (&u)[kUnroll]) {
-  constexpr int ROWS = kThreads / LG;
+  constexpr int ROWS = T / LG;
   const Groups e = groups_of<LG, PAIRS>(p, sd);
   const bool on = 8 * (int)(threadIdx.x % LG) < p.dim;
   const long long xb = at.b * sd.x_sb + at.s * sd.x_st;
@@ -98,10 +97,10 @@ __device__ __forceinline__ void load_heads(const NormParams& p, const Side& sd, 
     }
   }
 }
-template <int LG, int PAIRS>
+template <int T, int LG, int PAIRS>
 __device__ __forceinline__ void do_side(const NormParams& p, const Side& sd, long long token, const Place& place,
                                         uint4 (&u)[kUnroll]) {
-  constexpr int ROWS = kThreads / LG, UNROLL = kUnroll;
+  constexpr int ROWS = T / LG, UNROLL = kUnroll;
   const int first = threadIdx.x / LG;
   const Groups e = groups_of<LG, PAIRS>(p, sd);
   const bool on = 8 * (int)(threadIdx.x % LG) < p.dim;
@@ -148,7 +147,7 @@ __device__ __forceinline__ void do_side(const NormParams& p, const Side& sd, lon
   const float inv_dim = 1.f / (float)p.dim;
   // every lane takes every round (the shuffles need whole warps); heads past the last read nothing
   for (int h0 = 0; h0 < sd.heads; h0 += ROWS * UNROLL) {
-    if (h0 > 0) load_heads<LG, PAIRS>(p, sd, place, h0, u);
+    if (h0 > 0) load_heads<T, LG, PAIRS>(p, sd, place, h0, u);
 #pragma unroll
     for (int k = 0; k < UNROLL; ++k) {
       if (h0 + k * ROWS >= sd.heads) break;
@@ -204,26 +203,38 @@ __device__ __forceinline__ void do_side(const NormParams& p, const Side& sd, lon
   }
 }
 
-template <int LG, int PAIRS>
-__global__ void __launch_bounds__(kThreads, 6) k_qk_norm_rope(const __grid_constant__ NormParams p) {
+template <int T, int LG, int PAIRS>
+__global__ void __launch_bounds__(T, 768 / T) k_qk_norm_rope(const __grid_constant__ NormParams p) {
   pdl_wait();
   const long long n0 = (long long)p.side[0].batch * p.side[0].tokens, n1 = (long long)p.side[1].batch * p.side[1].tokens;
   const long long n = n0 > n1 ? n0 : n1;
   for (long long token = blockIdx.x; token < n; token += gridDim.x) {
     uint4 u0[kUnroll], u1[kUnroll];
     const Place at0 = place_of(p.side[0], token), at1 = place_of(p.side[1], token);
-    if (token < n0) load_heads<LG, PAIRS>(p, p.side[0], at0, 0, u0);
-    if (token < n1) load_heads<LG, PAIRS>(p, p.side[1], at1, 0, u1);
-    if (token < n0) do_side<LG, PAIRS>(p, p.side[0], token, at0, u0);
-    if (token < n1) do_side<LG, PAIRS>(p, p.side[1], token, at1, u1);
+    if (token < n0) load_heads<T, LG, PAIRS>(p, p.side[0], at0, 0, u0);
+    if (token < n1) load_heads<T, LG, PAIRS>(p, p.side[1], at1, 0, u1);
+    if (token < n0) do_side<T, LG, PAIRS>(p, p.side[0], token, at0, u0);
+    if (token < n1) do_side<T, LG, PAIRS>(p, p.side[1], token, at1, u1);
   }
 }
 
-template <int LG>
+template <int T, int LG>
 cudaError_t launch(const NormParams& p, unsigned grid, cudaStream_t stream) {
   return p.pairs == SVDQ_PAIRS_HALVES
-             ? launch_pdl(k_qk_norm_rope<LG, 1>, dim3(grid), dim3(kThreads), 0, stream, p)
-             : launch_pdl(k_qk_norm_rope<LG, 0>, dim3(grid), dim3(kThreads), 0, stream, p);
+             ? launch_pdl(k_qk_norm_rope<T, LG, 1>, dim3(grid), dim3(T), 0, stream, p)
+             : launch_pdl(k_qk_norm_rope<T, LG, 0>, dim3(grid), dim3(T), 0, stream, p);
+}
+// Threads to a token.  Few tokens: four warps, for the latency (one token of 24 + 24 heads of 128: 2.7 us, with one warp
+// 6.9).  With more, the SMs are filled by tokens, and fewer threads to each leave fewer of them without a head and load
+// the token's coefficients less often: 999 tokens of 16 + 4 heads of 72 5.0 us with four warps, 4.0 with two, 4.7 with
+// one; 18000 of 16 + 4 of 96 58, 44 and 37; 9216 of 24 + 24 of 128 44.3, 43.7 and 44.5.
+template <int LG>
+cudaError_t launch(const NormParams& p, int64_t tokens, int dev, cudaStream_t stream) {
+  const unsigned grid = (unsigned)(tokens < (1 << 20) ? tokens : (1 << 20));
+  const int64_t sms = device_sm_count(dev);
+  if (tokens <= 2 * sms) return launch<128, LG>(p, grid, stream);
+  const int lanes = (p.side[0].heads + p.side[1].heads) * LG;
+  return tokens >= 12 * sms && lanes <= 512 ? launch<32, LG>(p, grid, stream) : launch<64, LG>(p, grid, stream);
 }
 
 }  // namespace
@@ -298,14 +309,13 @@ extern "C" svdq_status svdq_qk_norm_rope(const svdq_norm_rope_args* q, const svd
   p.eps = eps;
   p.status = status;
   NvtxRange range("svdq/qk_norm_rope");
-  const unsigned grid = (unsigned)(tokens < (1 << 20) ? tokens : (1 << 20));
   const cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
-  if (dim <= 8) e = launch<1>(p, grid, s);
-  else if (dim <= 16) e = launch<2>(p, grid, s);
-  else if (dim <= 32) e = launch<4>(p, grid, s);
-  else if (dim <= 64) e = launch<8>(p, grid, s);
-  else if (dim <= 128) e = launch<16>(p, grid, s);
-  else e = launch<32>(p, grid, s);
+  if (dim <= 8) e = launch<1>(p, tokens, dev, s);
+  else if (dim <= 16) e = launch<2>(p, tokens, dev, s);
+  else if (dim <= 32) e = launch<4>(p, tokens, dev, s);
+  else if (dim <= 64) e = launch<8>(p, tokens, dev, s);
+  else if (dim <= 128) e = launch<16>(p, tokens, dev, s);
+  else e = launch<32>(p, tokens, dev, s);
   return e == cudaSuccess ? SVDQ_OK : SVDQ_ERR_CUDA;
 }

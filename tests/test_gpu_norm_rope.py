@@ -46,6 +46,23 @@ def test_heads_and_pairs(d, rot, pairs):
     assert torch.isfinite(oq).all()
 
 
+@pytest.mark.parametrize("pairs", ["interleaved", "halves"])
+@pytest.mark.parametrize("d,rot", [(8, 8), (40, 24), (64, 64), (128, 128), (256, 128)])
+@pytest.mark.parametrize("b,s,hq,hk", [(2, 148, 3, 1), (1, 297, 5, 2), (3, 592, 1, 1), (1, 1777, 17, 4), (2, 1000, 33, 3)])
+def test_threads_to_a_token(b, s, hq, hk, d, rot, pairs):
+    """Few tokens, some and many, with few heads and many: four warps to a token, two and one."""
+    import diffusion_transformer_w4a4_b200 as svdq
+
+    g = ac.generator(s + d)
+    qkv = ac.bf16(g, b, s, hq + hk, d)
+    q, k = qkv[:, :, :hq], qkv[:, :, hq:]
+    wq, wk = _weights(g, d)
+    table = ac.rope_table(s, rot, "cuda")
+    oq, ok = svdq.svdq_qk_norm_rope(q, k, wq, wk, rope=table, pairs=pairs)
+    ac.check(oq, *ac.norm_rope(q, wq, 1e-6, table, None, pairs))
+    ac.check(ok, *ac.norm_rope(k, wk, 1e-6, table, None, pairs))
+
+
 @pytest.mark.parametrize("b,s,hq,hk", [(1, 1, 1, 1), (1, 1, 24, 24), (3, 333, 16, 4), (2, 1025, 40, 1), (1, 5, 100, 3)])
 def test_fused_views_positions_in_place(b, s, hq, hk):
     import torch
