@@ -203,3 +203,35 @@ def test_block_table_streams_and_capture(tmp_path):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_many_calls_at_once():
+    """Every kind of launch (persistent, clusters, few tokens) on four streams at once: the bits of one call alone."""
+    import torch
+
+    import diffusion_transformer_w4a4_b200 as svdq
+
+    g = ac.generator(41)
+    calls = []
+    for M, K, N in ((3, 2048, 1024), (50, 2048, 768), (100, 4096, 512), (700, 512, 2048)):
+        lin, _ = _fp8(g, K, N)
+        x = ac.bf16(g, M, K)
+        calls.append(lambda lin=lin, x=x: lin(x))
+    for b, sq, sk, hq, hk, d in ((2, 1, 2000, 8, 4, 128), (1, 300, 4100, 6, 2, 128), (1, 100, 3000, 4, 4, 64),
+                                 (2, 1500, 200, 16, 16, 64)):
+        q, k, v = ac.bf16(g, b, sq, hq, d), ac.bf16(g, b, sk, hk, d), ac.bf16(g, b, sk, hk, d)
+        calls.append(lambda q=q, k=k, v=v: svdq.svdq_cross_attn(q, k, v))
+    q, k = ac.bf16(g, 2, 900, 5, 64), ac.bf16(g, 2, 900, 3, 64)
+    calls.append(lambda: torch.cat(svdq.svdq_qk_norm_rope(q, k), 2))
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    for r in range(8):
+        for i, c in enumerate(calls):  # a call always on one stream: a layer's workspace serves one call at a time
+            with torch.cuda.stream(streams[i % 4]):
+                got.append((i, c()))
+    torch.cuda.synchronize()
+    for i, y in got:
+        assert torch.equal(y, want[i]), i
+    assert int(svdq.attn_status().item()) == 0

@@ -202,6 +202,27 @@ def test_wait_limit_reports_and_recovers(M):
     _check(lin, x, lin.forward(x), qw, sw, b)
 
 
+@pytest.mark.parametrize("M,K,N", [(100, 4096, 512), (400, 6144, 1536), (2, 4096, 512)])
+def test_wait_limit_of_a_cluster(M, K, N):
+    """A wait that runs out in one CTA of a cluster: reported, the others leave too, and the next call is right."""
+    import torch
+
+    import diffusion_transformer_w4a4_b200 as svdq
+
+    lin, qw, sw, b = _layer(K, N, 31)
+    x = _x(ac.generator(9), M, K)
+    _check(lin, x, lin.forward(x), qw, sw, b)
+    try:
+        svdq.svdq_set_wait_limit(1)
+        lin.forward(x)
+        torch.cuda.synchronize()
+        st = lin.status(M)
+    finally:
+        svdq.svdq_set_wait_limit(0)
+    assert st == svdq.SVDQ_ERR_TIMEOUT
+    _check(lin, x, lin.forward(x), qw, sw, b)
+
+
 def test_refusals():
     import torch
 
