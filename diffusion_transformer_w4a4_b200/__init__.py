@@ -735,7 +735,7 @@ def svdq_fp8_pack(wcodes, wscales, bias=None) -> np.ndarray:
     if b is not None and b.shape != (N,):
         raise ValueError(f"expected a bias [{N}], got {b.shape}")
     size = svdq_fp8_packed_size(N, K)
-    blob = np.zeros(size, np.uint8)
+    blob = np.empty(size, np.uint8)
     _check(lib().svdq_fp8_pack(N, K, wcodes.ctypes.data, wscales.ctypes.data, None if b is None else b.ctypes.data,
                                blob.ctypes.data, size), "svdq_fp8_pack")
     return blob

@@ -79,6 +79,10 @@ bool f8_shape_ok(int64_t N, int64_t K) {
 // ------------------------------------------------------------------ quantizer
 // 16 lanes to a block of 128 inputs of one token, R blocks at a time, all asked for before the first is used: four where
 // there are enough to fill the SMs (4608 x 12288: 44 -> 37 us), one where there are few (the latency of one block).
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2(*(const __nv_bfloat162*)&a, *(const __nv_bfloat162*)&b);
+  return *(const uint32_t*)&m;
+}
 template <int R>
 __global__ void __launch_bounds__(kQuantThreads) k_fp8_quantize(const uint16_t* __restrict__ x, int64_t M, int K, int KB,
                                                               uint8_t* __restrict__ codes, float* __restrict__ scales,
@@ -107,30 +111,31 @@ __global__ void __launch_bounds__(kQuantThreads) k_fp8_quantize(const uint16_t* 
       ++m;
     }
   }
+  // The largest magnitude of each block, two elements at a time; a NaN stays out here and gives a NaN code.
+  float mx = 0.f;  // of block r in the lanes sub = r (mod R)
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const uint32_t w[4] = {u[r].x, u[r].y, u[r].z, u[r].w};
-    float v[8], mx = kAmaxMin;
+    uint32_t m = max_bf16x2(max_bf16x2(u[r].x & 0x7FFF7FFFu, u[r].y & 0x7FFF7FFFu),
+                            max_bf16x2(u[r].z & 0x7FFF7FFFu, u[r].w & 0x7FFF7FFFu));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float(w[e] << 16);
-      v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-      mx = fmaxf(mx, fmaxf(fabsf(v[2 * e]), fabsf(v[2 * e + 1])));  // a NaN stays out here and gives a NaN code
-    }
+    for (int o = 8; o > 0; o >>= 1) m = max_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float f = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    mx = (sub & (R - 1)) == r ? f : mx;
+  }
+  // One division for the R blocks, each in lanes of its own.
+  const float s_mine = __fdiv_rn(fmaxf(mx, kAmaxMin), kFp8Max), inv_mine = __fdiv_rn(1.f, s_mine);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float s = __fdiv_rn(mx, kFp8Max), inv = __fdiv_rn(1.f, s);
+  for (int r = 0; r < R; ++r) {
+    const float s = __shfl_sync(0xffffffffu, s_mine, r, 16), inv = __shfl_sync(0xffffffffu, inv_mine, r, 16);
     if (on[r]) {
-      uint32_t q[2];
+      const uint64_t inv2 = pack2(inv, inv);
+      const uint32_t w[4] = {u[r].x, u[r].y, u[r].z, u[r].w};
+      uint32_t q[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h] * inv, v[4 * h + 1] * inv), __NV_SATFINITE,
-                                                     __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * h + 2] * inv, v[4 * h + 3] * inv),
-                                                     __NV_SATFINITE, __NV_E4M3);
-        q[h] = lo | (hi << 16);
-      }
-      if (SVDQ_INB(status, at[r], 8, M * K)) *(uint2*)(codes + at[r]) = make_uint2(q[0], q[1]);
+      for (int e = 0; e < 4; ++e)
+        q[e] = __nv_cvt_float2_to_fp8x2(unpack2(mul2(pack2(w[e] << 16, w[e] & 0xFFFF0000u), inv2)), __NV_SATFINITE,
+                                        __NV_E4M3);
+      if (SVDQ_INB(status, at[r], 8, M * K)) *(uint2*)(codes + at[r]) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
       if (sub == 0 && SVDQ_INB(status, 4 * sc[r], 4, 4 * M * ld)) scales[sc[r]] = s;
     }
   }
@@ -1036,10 +1041,15 @@ svdq_status svdq_fp8_pack(int64_t N, int64_t K, const uint8_t* wcodes, const flo
   const int64_t ns = ((N + kBlk - 1) / kBlk) * ((K + kBlk - 1) / kBlk);
   for (int64_t i = 0; i < ns; ++i)
     if (!(wscales[i] >= 0.f) || !std::isfinite(wscales[i])) return SVDQ_ERR_INVALID_ARG;
-  for (int64_t i = 0; i < N * K; ++i)
-    if ((wcodes[i] & 0x7F) == 0x7F) return SVDQ_ERR_INVALID_ARG;  // E4M3 NaN
+  for (int64_t i = 0; i < N * K;) {  // E4M3 NaN; a stretch at a time, which the compiler turns into vectors
+    const int64_t end = std::min(N * K, i + 4096);
+    int bad = 0;
+    for (; i < end; ++i) bad |= (wcodes[i] & 0x7F) == 0x7F;
+    if (bad) return SVDQ_ERR_INVALID_ARG;
+  }
   uint8_t* blob = (uint8_t*)blob_v;
-  std::memset(blob, 0, b.total);
+  std::memset(blob, 0, b.wcodes);
+  std::memset(blob + b.wcodes + (size_t)N * K, 0, b.total - b.wcodes - (size_t)N * K);
   float* bf = (float*)(blob + b.bias);
   for (int64_t n = 0; n < N; ++n) bf[n] = bias ? host::bf16_to_f32(bias[n]) : 0.f;
   const int64_t kb = (K + kBlk - 1) / kBlk, ld = f8_scale_ld(K);
