@@ -6,7 +6,7 @@
 // The floor 2^-100 keeps s and 1/s normal numbers, so a block of zeros (or of subnormals) needs no branch.
 // Two kernels per forward:
 //   k_fp8_quantize  16 lanes to a block of 128, the maximum by shuffles; bound by memory (2 + 1 bytes an element:
-//                   4608 x 3072 9.9 us, 4.3 TB/s; 4608 x 12288 36 us, 4.7 TB/s).
+//                   4608 x 3072 8.8 us, 4.8 TB/s; 4608 x 12288 35 us, 4.9 TB/s).
 //   the product     tcgen05.mma kind::f8f6f4 over one block of 128 inputs at a time into a tensor-memory accumulator of its
 //                   own; the scales differ from block to block, so warps fold each finished block into sums in registers,
 //                   acc += (s_x s_w) d, while the tensor cores work on the next.  The weight scale is one number for a
@@ -78,7 +78,7 @@ bool f8_shape_ok(int64_t N, int64_t K) {
 
 // ------------------------------------------------------------------ quantizer
 // 16 lanes to a block of 128 inputs of one token, R blocks at a time, all asked for before the first is used: four where
-// there are enough to fill the SMs (4608 x 12288: 44 -> 37 us), one where there are few (the latency of one block).
+// there are enough to fill the SMs (4608 x 12288: 35 us; one at a time 44), one where there are few (the latency of one block).
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 m = __hmax2(*(const __nv_bfloat162*)&a, *(const __nv_bfloat162*)&b);
   return *(const uint32_t*)&m;
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_gemm_fp8_few(const __grid_co
     tc_fence_after();
     tmem_dealloc(tmem, T::kCols);
   }
-  const bool good = *abort_flag == 0;  // after an expired wait nothing is stored
+  const bool good = *abort_flag == 0;  // after an expired wait this CTA stores nothing
   if (p.splits == 1) {
     const int n = nt * 128 + threadIdx.x;
     if (good && warp < 4 && n < p.N && SVDQ_INB(p.status, 4ll * n, 4, 4ll * p.N)) {
