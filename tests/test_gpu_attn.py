@@ -156,6 +156,31 @@ def test_masked_keys_have_no_influence(sq, hq, hk, d, bad):
     assert (o == 0.25).all()
 
 
+@pytest.mark.parametrize("sq,h,d", [(300, 4, 128), (100, 3, 128), (100, 3, 64), (2, 4, 72), (300, 6, 40)])
+def test_masked_keys_have_no_influence_on_split_keys(sq, h, d):
+    """The same where clusters split the keys: NaN and infinities behind a length, and behind masks, of whole tiles too."""
+    import torch
+
+    import diffusion_transformer_w4a4_b200 as svdq
+
+    g = ac.generator(25)
+    b, sk = 2, 3000
+    q, k, v = ac.bf16(g, b, sq, h, d), ac.bf16(g, b, sk, h, d), ac.bf16(g, b, sk, h, d)
+    mask = torch.rand(b, sk, generator=g, device="cuda") < 0.7
+    mask[:, 256:1100] = False
+    kv_len = torch.tensor([2900, 1301], dtype=torch.int32, device="cuda")
+    want = svdq.svdq_cross_attn(q, k, v, kv_len=kv_len, kv_mask=mask)
+    ac.check(want, *ac.attention(q, k, v, kv_len, mask, ac.inv_sqrt(d)))
+    by_len = svdq.svdq_cross_attn(q, k, v, kv_len=kv_len)
+    past = torch.arange(sk, device="cuda")[None] >= kv_len[:, None]
+    for bad in (float("nan"), float("inf"), -3.0e38):
+        kk, vv = k.clone(), v.clone()
+        kk[past], vv[past] = bad, bad
+        assert torch.equal(by_len, svdq.svdq_cross_attn(q, kk, vv, kv_len=kv_len))
+        kk[~mask], vv[~mask] = bad, bad
+        assert torch.equal(want, svdq.svdq_cross_attn(q, kk, vv, kv_len=kv_len, kv_mask=mask))
+
+
 def test_nan_in_a_counting_key_shows():
     import torch
 
