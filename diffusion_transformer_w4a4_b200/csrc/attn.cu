@@ -24,7 +24,7 @@
 //                take a quarter of the time; the other quarters' P is zero there, and the quarters are joined too.
 // What bounds it: with many rows the chain S -> exponentials -> P -> product, about 3200 clocks for a key tile of both
 // streams against 2048 of products (heads of 128: 24 x 4096 x 4608 in 200 us, 1.16 PFLOP/s); with few rows latency
-// (2 x 24 heads of one token over 4096 keys: 13.9 us, 34 MB of keys and values at 2.4 TB/s).  A quarter of the
+// (2 x 24 heads of one token over 4096 keys: 13.2 us, 34 MB of keys and values at 2.5 TB/s).  A quarter of the
 // exponentials are computed by a polynomial, as the special-function unit is the busiest: 24 x 4096 x 4608 in 195-200 us
 // against 217 with none of them, 223 with an eighth and 218 with a half.
 // Rows of a tile are (token, query head of the group) pairs, so heads that share keys share their tiles.
@@ -348,11 +348,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
   using G = Geo<DC>;
   constexpr bool PAIR = MODE == kPairs || MODE == kSplitPairs, QUART = MODE == kQuarter;
   constexpr bool JOIN = MODE != kPairs;  // results of several CTAs or streams are joined at the end
-  constexpr int SLOTS = G::kSlots;
+  // Query tiles; key and value tiles in flight.  Where there is one query tile the ring has the other's place (2 x 24 heads
+  // of one token over 4096 keys: 13.9 -> 13.2 us).
+  constexpr int QT = PAIR ? 2 : 1, SLOTS = G::kSlots + 2 - QT;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* sm_q = smem;                   // [2][tile]
-  uint8_t* sm_kv = smem + 2 * G::kTile;   // [SLOTS][tile]
+  uint8_t* sm_q = smem;                    // [QT][tile]
+  uint8_t* sm_kv = smem + QT * G::kTile;   // [SLOTS][tile]
   uint8_t* sm_stage = sm_kv + SLOTS * G::kTile;      // [8][4 KiB]
   float* sm_m = (float*)sm_stage;                    // [2][128]
   float* sm_l = sm_m + 256;                          // [2][128]
