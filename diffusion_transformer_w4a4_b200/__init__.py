@@ -195,18 +195,21 @@ def _stream(stream) -> int | None:
     return int(getattr(stream, "cuda_stream", stream))
 
 
-def _stream_context(stream):
-    """`stream` (a torch stream or a raw handle) as the current stream."""
+def _stream_context(stream, device):
+    """`stream` (a torch stream, or a raw handle of one of `device`) as the current stream of `device`."""
     torch = _torch()
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
-                             torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream))))
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+    if stream.device != device:
+        raise ValueError(f"a stream of {stream.device} for work on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _empty_like(x, stream):
     """An output like x, of the memory of the stream that will write it."""
-    if stream is None:
+    if stream is None or not x.is_cuda:  # (a tensor of the host is refused later, with the others' checks)
         return _torch().empty_like(x)
-    with _stream_context(stream):
+    with _stream_context(stream, x.device):
         return _torch().empty_like(x)
 
 
@@ -810,7 +813,7 @@ class Fp8Linear:
         if stream is not None:
             if out is None:
                 _check_input(x, self.K, self.device)
-                with _stream_context(stream):
+                with _stream_context(stream, self.device):
                     out = _torch().empty(x.numel() // self.K, self.N, dtype=x.dtype, device=self.device)
             stream = _stream(stream)
         forward = (_calls_module or _calls()).fp8_forward

@@ -20,14 +20,15 @@ from . import SVDQ_OK, _layer_device, _stream_context, svdq_cross_attn, svdq_mlp
 
 
 def _on_stream(f):
-    """The method with its `stream` argument made the current stream: its intermediates then belong to that stream."""
+    """The method with its `stream` argument made the current stream of the object's device: its intermediates then
+    belong to that stream."""
 
     @functools.wraps(f)
-    def g(*args, stream=None, **kw):
+    def g(self, *args, stream=None, **kw):
         if stream is None:
-            return f(*args, **kw)
-        with _stream_context(stream):
-            return f(*args, **kw)
+            return f(self, *args, **kw)
+        with _stream_context(stream, self.device):
+            return f(self, *args, **kw)
 
     return g
 
@@ -64,7 +65,7 @@ class SelfAttention:
         self.dim = _fits(heads, to_qkv.N, 3, "to_qkv")
         if to_out.K != heads * self.dim or to_out.device != to_qkv.device:
             raise ValueError("to_out does not take to_qkv's heads")
-        self.to_qkv, self.to_out, self.heads = to_qkv, to_out, heads
+        self.to_qkv, self.to_out, self.heads, self.device = to_qkv, to_out, heads, to_out.device
         self.q_norm, self.k_norm, self.eps, self.pairs = q_norm, k_norm, eps, pairs
 
     @_on_stream
@@ -96,6 +97,7 @@ class CrossAttention:
         if to_out.K != heads * self.dim or not (to_q.device == to_kv.device == to_out.device):
             raise ValueError("to_out does not take to_q's heads")
         self.to_q, self.to_kv, self.to_out, self.heads, self.kv_heads = to_q, to_kv, to_out, heads, kv_heads
+        self.device = to_out.device
         self.q_norm, self.k_norm, self.eps, self.pairs = q_norm, k_norm, eps, pairs
 
     @_on_stream
@@ -132,7 +134,7 @@ class FluxBlock:
         self.up, self.down = layers[prefix + "ff.net.0.proj"], layers[prefix + "ff.net.2"]
         if svdq_mlp_fusable(self.up.handle, self.down.handle) != SVDQ_OK:
             raise ValueError("the MLP pair's shapes or formats cannot be fused (both NVFP4, static scale)")
-        self.theta, self._ropes = theta, []
+        self.theta, self._ropes, self.device = theta, [], self.up.device
 
     def _table(self, tokens: int):
         """Cosines and sines of the first `tokens` rows; a longer table than any before is made once, and waited for."""
