@@ -785,8 +785,9 @@ class Fp8Linear:
     current CUDA device), from E4M3 weight codes u8 [N,K] (svdq_fp8_prepare, or a
     checkpoint's own), their scales f32 [ceil(N/128), ceil(K/128)] and an optional
     bf16 bias (bits); `forward(x)` maps bf16 [M, K] to bf16 [M, N], enqueued with the
-    layer's device current.  Workspaces are cached per token count and used by one
-    call at a time (calls on several streams take one layer object each)."""
+    layer's device current.  Workspaces are cached per token count, belong to the
+    stream that used them first and are used by one call at a time (calls on several
+    streams take one layer object each)."""
 
     def __init__(self, wcodes, wscales, bias=None, device=None):
         import torch
@@ -797,30 +798,28 @@ class Fp8Linear:
         with torch.cuda.device(self.device):
             self.handle = svdq_fp8_layer_create(self.blob, self.blob.numel(), self.N, self.K)
         self._handle = self.handle.value
-        self._ws = {}
+        self._blob_stream = torch.cuda.current_stream(self.device).cuda_stream
+        self._ws = {}  # token count: (workspace, handle of the stream whose memory it is, weights, theirs)
 
     def workspace_size(self, M: int) -> int:
         return svdq_fp8_workspace_size(self.handle, M)
 
     def workspace(self, M: int):
-        import torch
-
         if M not in self._ws:
-            self._ws[M] = torch.empty(self.workspace_size(M), dtype=torch.uint8, device=self.device)
-        return self._ws[M]
+            torch = _torch()
+            ws = torch.empty(self.workspace_size(M), dtype=torch.uint8, device=self.device)
+            self._ws[M] = ws, torch.cuda.current_stream(self.device).cuda_stream, self.blob, self._blob_stream
+        return self._ws[M][0]
 
     def forward(self, x, out=None, stream=None):
-        if stream is not None:
-            if out is None:
-                _check_input(x, self.K, self.device)
-                with _stream_context(stream, self.device):
-                    out = _torch().empty(x.numel() // self.K, self.N, dtype=x.dtype, device=self.device)
-            stream = _stream(stream)
+        if stream is not None:  # what the call allocates, a workspace among it, is memory of the stream that writes it
+            with _stream_context(stream, self.device):
+                return self.forward(x, out)
         forward = (_calls_module or _calls()).fp8_forward
-        y = forward(self._handle, self.N, self.K, self.device.index, self._ws, x, out, stream)
+        y = forward(self._handle, self.N, self.K, self.device.index, self._ws, x, out)
         if y is None:  # the first call with this many tokens
             self.workspace(x.numel() // self.K)
-            y = forward(self._handle, self.N, self.K, self.device.index, self._ws, x, out, stream)
+            y = forward(self._handle, self.N, self.K, self.device.index, self._ws, x, out)
         return y
 
     __call__ = forward

@@ -104,6 +104,15 @@ long long integer(PyObject* o) {
   return v;
 }
 
+// Memory of stream `owner` that a call on `stream` uses: the allocator hands it to nobody before the call is done, though it
+// be dropped earlier.  A raw handle's stream is not noted, as it may be destroyed before the memory is freed.
+void note_use(const at::Tensor& t, void* owner, const c10::cuda::CUDAStream& stream) {
+  const cudaStream_t handle = stream.stream();
+  if ((void*)handle == owner) return;
+  if (handle && stream == c10::cuda::getStreamFromExternal(handle, stream.device_index())) return;
+  t.record_stream(stream);
+}
+
 // call() with `device` current; a status other than SVDQ_OK raises.
 template <class F>
 void run(const c10::Device& device, const char* where, F&& call) {
@@ -253,10 +262,10 @@ PyObject* cross_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// fp8_forward(handle, N, K, device index, workspaces by token count, x, out, stream) -> y, or None where there is no
-// workspace yet
+// fp8_forward(handle, N, K, device index, memory by token count, x, out) -> y on the device's current stream, or None
+// where there is no workspace yet.  The memory: (workspace, handle of its stream, weights, handle of theirs).
 PyObject* fp8_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 8, [&]() -> PyObject* {
+  return guarded(n, 7, [&]() -> PyObject* {
     const auto* layer = (const svdq_fp8_layer*)PyLong_AsVoidPtr(a[0]);
     const int64_t N = integer(a[1]), K = integer(a[2]);
     const c10::Device device(c10::DeviceType::CUDA, (c10::DeviceIndex)integer(a[3]));
@@ -274,7 +283,10 @@ PyObject* fp8_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (PyErr_Occurred()) throw PyError();
       Py_RETURN_NONE;
     }
-    const at::Tensor& ws = tensor("workspace", w);
+    if (!PyTuple_Check(w) || PyTuple_GET_SIZE(w) != 4) refuse("memory of ", M, " tokens: expected a tuple of four");
+    const at::Tensor &ws = tensor("workspace", PyTuple_GET_ITEM(w, 0)), &blob = tensor("weights", PyTuple_GET_ITEM(w, 2));
+    void *const ws_owner = PyLong_AsVoidPtr(PyTuple_GET_ITEM(w, 1)), *const blob_owner = PyLong_AsVoidPtr(PyTuple_GET_ITEM(w, 3));
+    if (PyErr_Occurred()) throw PyError();
     at::Tensor made;
     const at::Tensor* y = &made;
     if (a[6] == Py_None) {
@@ -284,9 +296,11 @@ PyObject* fp8_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (y->scalar_type() != at::kBFloat16 || y->device() != device || !y->is_contiguous() || y->numel() != M * N)
         refuse("expected a contiguous bf16 output [", M, ", ", N, "] on ", device);
     }
-    void* stream = stream_of(a[7], device);
+    const c10::cuda::CUDAStream stream = c10::cuda::getCurrentCUDAStream(device.index());
+    note_use(ws, ws_owner, stream);
+    note_use(blob, blob_owner, stream);
     run(device, "svdq_fp8_forward", [&] {
-      return g_fp8(layer, x.data_ptr(), M, y->data_ptr(), ws.data_ptr(), (size_t)ws.numel(), stream);
+      return g_fp8(layer, x.data_ptr(), M, y->data_ptr(), ws.data_ptr(), (size_t)ws.numel(), (void*)stream.stream());
     });
     return a[6] == Py_None ? THPVariable_Wrap(made) : Py_NewRef(a[6]);
   });

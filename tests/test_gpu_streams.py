@@ -1,0 +1,115 @@
+"""Memory that a layer allocates for a call on another stream than the current one: it is that stream's, so work that is
+still pending on the current stream never shares it, and a dropped layer's memory waits for every stream that used it."""
+import numpy as np
+import pytest
+
+import attn_cases as ac
+
+pytestmark = pytest.mark.gpu
+
+CYCLES = 200_000_000  # about a tenth of a second
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    import torch
+
+    import diffusion_transformer_w4a4_b200 as svdq
+    from diffusion_transformer_w4a4_b200 import build
+
+    build.build()
+    assert torch.cuda.is_available()
+    assert svdq.svdq_device_check(0) == svdq.SVDQ_OK, "needs an sm_100a device"
+    torch.cuda.set_device(0)
+
+
+def _fp8(K, N, seed):
+    import torch
+
+    import diffusion_transformer_w4a4_b200 as svdq
+
+    w = ac.bf16(ac.generator(seed), N, K, scale=0.05)
+    return svdq.Fp8Linear(*svdq.svdq_fp8_prepare(w.view(torch.int16).cpu().numpy().view(np.uint16)), device="cuda:0")
+
+
+def _on_side(torch, side, M, K):
+    """Inputs that live on `side`, complete there."""
+    with torch.cuda.stream(side):
+        x = ac.bf16(ac.generator(M), M, K)
+    torch.cuda.synchronize()
+    return x
+
+
+def _pending_fill(torch, sizes):
+    """Freed blocks of the current stream that it has yet to write; their addresses."""
+    blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda._sleep(CYCLES)
+    for b in blocks:
+        b.fill_(0xA5)
+    return [b.data_ptr() for b in blocks]
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_first_call_on_a_side_stream_keeps_its_workspace(raw):
+    import torch
+
+    M, K, N = 700, 2048, 1024
+    want_codes, want_scales = ac.fp8_quantize(_on_side(torch, torch.cuda.Stream(), M, K))
+    lin, side = _fp8(K, N, 1), torch.cuda.Stream()
+    x = _on_side(torch, side, M, K)
+    torch.cuda.empty_cache()
+    freed = _pending_fill(torch, [lin.workspace_size(M), 2 * M * N])
+    y = lin.forward(x, stream=side.cuda_stream if raw else side)  # its first call with M tokens
+    torch.cuda.synchronize()  # the fill has run by now
+    assert lin.workspace(M).data_ptr() not in freed and y.data_ptr() not in freed
+    act = lin.read_act(M)
+    assert torch.equal(torch.from_numpy(act["codes"]).view(torch.float8_e4m3fn).double().cuda(), want_codes)
+    np.testing.assert_array_equal(act["scales"], want_scales.cpu().numpy())
+    assert lin.status(M) == 0 and torch.equal(y, lin.forward(x))
+
+
+def test_dropped_layer_waits_for_the_other_stream():
+    """A layer and its workspace, memory of the current stream, used on another one and dropped while that still works:
+    neither is handed out."""
+    import torch
+
+    M, K, N = 700, 2048, 1024
+    lin, side = _fp8(K, N, 2), torch.cuda.Stream()
+    x = _on_side(torch, side, M, K)
+    want = lin.forward(x)
+    out = torch.empty_like(want)
+    used = [(t.data_ptr(), t.numel()) for t in (lin.workspace(M), lin.blob)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(CYCLES)
+        lin.forward(x, out=out)
+    del lin
+    again = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in used]
+    for t in again:
+        assert all(t.data_ptr() + t.numel() <= at or t.data_ptr() >= at + n for at, n in used)
+        t.fill_(0xFF)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_destroyed_raw_stream_before_the_layer():
+    """A raw handle's stream destroyed before the layer is dropped: nothing is recorded on it."""
+    import ctypes
+
+    import torch
+
+    M, K, N = 300, 512, 256
+    rt = ctypes.CDLL("libcudart.so.12")
+    lin = _fp8(K, N, 3)
+    x = ac.bf16(ac.generator(M), M, K)
+    want = lin.forward(x)
+    torch.cuda.synchronize()
+    handle = ctypes.c_void_p()
+    assert rt.cudaStreamCreate(ctypes.byref(handle)) == 0
+    got = lin.forward(x, stream=handle.value)
+    torch.cuda.synchronize()
+    equal = torch.equal(got, want)
+    del got, lin  # (what the call allocated goes back before its stream does)
+    torch.cuda.synchronize()
+    assert rt.cudaStreamDestroy(handle) == 0
+    assert equal
