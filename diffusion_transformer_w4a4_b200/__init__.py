@@ -13,6 +13,7 @@ steps between a block's projections, take torch tensors [batch, tokens, heads, d
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -203,6 +204,11 @@ def _stream_context(stream, device):
     if stream.device != device:
         raise ValueError(f"a stream of {stream.device} for work on {device}")
     return torch.cuda.stream(stream)
+
+
+def _on(stream, device):
+    """The stream that a call works on as the current one: what the call allocates is its memory."""
+    return contextlib.nullcontext() if stream is None else _stream_context(stream, device)
 
 
 def _empty_like(x, stream):
@@ -445,10 +451,9 @@ class SvdqLinear:
 
         _check_input(x, self.K, self.device)
         M = x.numel() // self.K
-        y = out if out is not None else torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
-        ws = self.workspace(M)
-        with torch.cuda.device(self.device):
-            svdq_forward(self.handle, x, M, y, ws, stream)
+        with torch.cuda.device(self.device), _on(stream, self.device):
+            y = out if out is not None else torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
+            svdq_forward(self.handle, x, M, y, self.workspace(M), stream)
         return y
 
     __call__ = forward
@@ -558,8 +563,8 @@ class AwqLinear:
 
         _check_input(x, self.K, self.device)
         M = x.numel() // self.K
-        y = out if out is not None else torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
-        with torch.cuda.device(self.device):
+        with torch.cuda.device(self.device), _on(stream, self.device):
+            y = out if out is not None else torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
             svdq_awq_forward(self.handle, x, M, y, stream)
         return y
 
@@ -670,26 +675,23 @@ class W8A8Linear:
     def quantize_act(self, x, M: int, stream=None):
         import torch
 
-        ws = self.workspace(M)
-        with torch.cuda.device(self.device):
-            svdq_w8a8_quantize_act(self.handle, x, M, ws, stream)
+        with torch.cuda.device(self.device), _on(stream, self.device):
+            svdq_w8a8_quantize_act(self.handle, x, M, self.workspace(M), stream)
 
     def gemm(self, M: int, y, stream=None):
         import torch
 
-        ws = self.workspace(M)
-        with torch.cuda.device(self.device):
-            svdq_w8a8_gemm(self.handle, M, y, ws, stream)
+        with torch.cuda.device(self.device), _on(stream, self.device):
+            svdq_w8a8_gemm(self.handle, M, y, self.workspace(M), stream)
 
     def forward(self, x, out=None, stream=None):
         import torch
 
         _check_input(x, self.K, self.device)
         M = x.numel() // self.K
-        y = out if out is not None else torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
-        ws = self.workspace(M)
-        with torch.cuda.device(self.device):
-            svdq_w8a8_forward(self.handle, x, M, y, ws, stream)
+        with torch.cuda.device(self.device), _on(stream, self.device):
+            y = out if out is not None else torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
+            svdq_w8a8_forward(self.handle, x, M, y, self.workspace(M), stream)
         return y
 
     __call__ = forward

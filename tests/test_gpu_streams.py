@@ -113,3 +113,41 @@ def test_destroyed_raw_stream_before_the_layer():
     torch.cuda.synchronize()
     assert rt.cudaStreamDestroy(handle) == 0
     assert equal
+
+
+def _older_layer(kind, N, K):
+    import numpy as np
+
+    import diffusion_transformer_w4a4_b200 as svdq
+
+    g = np.random.default_rng(5)
+    bits = lambda a: (a.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    W, X = bits(g.standard_normal((N, K)) * 0.05), bits(g.standard_normal((64, K)))
+    if kind == "awq":
+        return svdq.AwqLinear(svdq.svdq_awq_prepare(W, None, X), device="cuda:0")
+    if kind == "w8a8":
+        return svdq.W8A8Linear(*svdq.svdq_w8a8_prepare(W), device="cuda:0")
+    amax = np.abs((X.astype(np.uint32) << 16).view(np.float32)).max(0)
+    return svdq.SvdqLinear(svdq.svdq_prepare(W, None, amax, 0.5, 32, kind), device="cuda:0")
+
+
+@pytest.mark.parametrize("kind", ["nvfp4", "int4", "w8a8", "awq"])
+def test_first_call_on_a_side_stream_of_the_other_layers(kind):
+    """Workspace, its initialisation and output on the given stream: right at once, whatever the current one has yet to do."""
+    import torch
+
+    M, K, N = 300, 512, 384
+    lin, side = _older_layer(kind, N, K), torch.cuda.Stream()
+    x = _on_side(torch, side, M, K)
+    torch.cuda.empty_cache()
+    sizes = [2 * M * N] if kind == "awq" else [2 * M * N, 1 << 20]
+    freed = _pending_fill(torch, sizes)
+    y = lin.forward(x, stream=side)
+    side.synchronize()
+    first = y.cpu()  # (on the current stream, behind the fill)
+    assert y.data_ptr() not in freed
+    if kind != "awq":
+        assert lin.workspace(M).data_ptr() not in freed
+    torch.cuda.synchronize()
+    assert torch.equal(first, lin.forward(x).cpu())
+    assert (lin.status() if kind == "awq" else lin.status(M)) == 0
