@@ -54,6 +54,7 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 // kernel issues about as long as it moves data, so instructions count.
 // `u` holds the first heads' elements, asked for before anything else of the token.
 constexpr int kUnroll = 3;  // heads of a lane in flight for each side
+constexpr float kLeast = 0x1p-100f;  // least mean square that is taken as it comes: what its squares lose is below 2^-141
 struct Place {
   int b, s;
 };
@@ -170,7 +171,32 @@ __device__ __forceinline__ void do_side(const NormParams& p, const Side& sd, lon
       float ss = sp.x + sp.y;
 #pragma unroll
       for (int o = LG / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      float inv = rsqrtf(fmaf(ss, inv_dim, p.eps));
+      const float t = fmaf(ss, inv_dim, p.eps);
+      float inv = rsqrtf(t);
+      if (__any_sync(0xffffffffu, !(t >= kLeast && t < INFINITY))) {
+        // Past binary32, or so small that squares lost their bits: the same on 2^-96 x or 2^96 x.  On 2^96 x, which is exact,
+        // the head goes on; 2^-96 goes to the root instead, as the smaller elements would lose bits.  (The vote costs
+        // 0.3 us of the 44 for a block of 9216 tokens; a branch for each head without it 2, the heads done again after the
+        // round 1.)
+        const float by = t < kLeast ? 0x1p96f : (t < INFINITY ? 1.f : 0x1p-96f);
+        const uint64_t by2 = pack2(by, by);
+        uint64_t q2 = 0;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const uint64_t a = mul2(lo[g], by2), c = mul2(hi[g], by2);
+          q2 = fma2(a, a, q2);
+          q2 = fma2(c, c, q2);
+          if (by > 1.f) {
+            lo[g] = a;
+            hi[g] = c;
+          }
+        }
+        const float2 qp = unpack2(q2);
+        float qs = qp.x + qp.y;
+#pragma unroll
+        for (int o = LG / 2; o > 0; o >>= 1) qs += __shfl_xor_sync(0xffffffffu, qs, o);
+        inv = rsqrtf(fmaf(qs, inv_dim, p.eps * by * by)) * (by < 1.f ? by : 1.f);
+      }
       if (bad) inv = __int_as_float(0x7FC00000);
       const uint64_t inv2 = pack2(inv, inv);
       float2 y[2][2];  // [g][0] of the firsts of two pairs, [g][1] of the seconds

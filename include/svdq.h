@@ -499,7 +499,8 @@ typedef struct svdq_norm_rope_args {
 #define SVDQ_PAIRS_HALVES 1      /* (i, i + rot_dim/2) */
 
 /* y = rotate(weight * x / sqrt(mean x^2 + eps)) for each head of q and k (either
- * may be NULL), one launch: binary32 throughout, rounded once to bf16.  The
+ * may be NULL), one launch: binary32 throughout (a mean square that binary32 does
+ * not hold is taken of x times a power of two), rounded once to bf16.  The
  * rotation takes the pair (a, c) of the first rot_dim elements of a head to
  * (a cos - c sin, a sin + c cos) with the token's row of `rope`.  dim % 8 == 0,
  * 8 <= dim <= 256; rot_dim % 8 == 0, 0 <= rot_dim <= dim (ignored without rope);
