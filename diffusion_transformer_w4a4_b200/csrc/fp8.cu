@@ -26,6 +26,7 @@
 #include <cstring>
 #include <mutex>
 #include <new>
+#include <type_traits>
 
 #include "sm100.cuh"
 #include "svdq_internal.h"
@@ -36,6 +37,7 @@ struct svdq_fp8_layer {
   const float* bias;     // [N]
   const float* wscales;  // [NB, KB]
   const uint8_t* wcodes;  // [N, K]
+  const int* far;         // a scale above kFarScale is among them
   CUtensorMap map_w[3];  // boxes of 256, 128 and 64 rows
 };
 
@@ -45,12 +47,15 @@ namespace {
 constexpr int kBlk = 128;
 constexpr float kFp8Max = 448.f;
 constexpr float kAmaxMin = 0x1p-100f;
+// Weight scales above this may take the product of the scales past binary32; below it none does, as s_x is at most the
+// largest bf16 / 448 (or infinite, with a NaN among the codes).
+constexpr float kFarScale = 448.f;
 constexpr int kQuantThreads = 256;
 
 // Scales of a row (of X, or of a block of 128 rows of W): one per block of 128 inputs, padded to whole 16 bytes.
 int64_t f8_scale_ld(int64_t K) { return ((K + kBlk - 1) / kBlk + 3) / 4 * 4; }
 struct F8Blob {
-  size_t bias, wscales, wcodes, total;
+  size_t bias, wscales, wcodes, far, total;
 };
 F8Blob f8_blob_layout(int64_t N, int64_t K) {
   const int64_t nb = (N + kBlk - 1) / kBlk, kb = f8_scale_ld(K);
@@ -58,7 +63,8 @@ F8Blob f8_blob_layout(int64_t N, int64_t K) {
   b.bias = 0;
   b.wscales = align_up((size_t)N * 4, kAlign);
   b.wcodes = align_up(b.wscales + (size_t)(nb * kb) * 4, kAlign);
-  b.total = align_up(b.wcodes + (size_t)N * K, kAlign);
+  b.far = align_up(b.wcodes + (size_t)N * K, kAlign);
+  b.total = b.far + kAlign;
   return b;
 }
 struct F8Ws {
@@ -173,6 +179,7 @@ struct F8Params {
   int M, N, KB, NB, m_tiles, num_tiles, splits, per;  // per: blocks of 128 inputs of a CTA
   const float* sx;  // [M, ld]
   const float* sw;  // [NB, ld]
+  const int* far;
   int ld;
   const float* bias;
   uint16_t* Y;
@@ -316,6 +323,25 @@ __device__ __forceinline__ void fold64(uint32_t t, float s, float* a) {
       : "memory");
 }
 
+// Where s_x s_w is past binary32 although the block's sum d may be small or 0: d is multiplied by the smaller scale in
+// tensor memory first, and the fold takes the larger.  (Both are at least 1 there, or the input holds an infinity.)  Tiles
+// have a loop of their own for layers that can come to this: the test in the common one, once for four blocks, cost
+// 4608 x 3072 x 12288 5 us.
+__device__ __forceinline__ bool past_f32(float s) { return !(s <= 3.402823466e38f); }
+template <class Factor>  // factor(column)
+__device__ __forceinline__ void scale_columns(uint32_t t, int cols, Factor&& factor) {
+#pragma unroll 1
+  for (int c = 0; c < cols; c += 16) {
+    uint32_t d[16];
+    tmem_ld_32x32b_x16(t + c, d);
+    tmem_ld_wait_regs(d);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) d[i] = __float_as_uint(__uint_as_float(d[i]) * factor(c + i));
+    tmem_st_32x32b_x16(t + c, d);
+  }
+  tmem_st_wait();
+}
+
 template <int BN, bool SPLIT>
 __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_constant__ F8Maps maps,
                                                              const __grid_constant__ F8Params p) {
@@ -449,38 +475,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
     bool ok = true;
     float4 xn = make_float4(0.f, 0.f, 0.f, 0.f), wn = xn;  // the next four blocks' scales, asked for four folds ahead
     fetch(xn, wn);
-    for (int tile = tile0; tile < p.num_tiles && ok; tile += step) {
-      const int m0 = mt * 128 + 32 * q;
-      const int n0 = nt * BN + FC * h;
-      // The bias is added at the end; bring it near now.
-      if (8 * lane < FC && n0 + 8 * lane < p.N)
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bias + n0 + 8 * lane));
-      float acc[FC];
+    // far: a product of scales may be past binary32.
+    auto tiles = [&](auto far) {
+      for (int tile = tile0; tile < p.num_tiles && ok; tile += step) {
+        const int m0 = mt * 128 + 32 * q;
+        const int n0 = nt * BN + FC * h;
+        // The bias is added at the end; bring it near now.
+        if (8 * lane < FC && n0 + 8 * lane < p.N)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(p.bias + n0 + 8 * lane));
+        float acc[FC];
 #pragma unroll
-      for (int i = 0; i < FC; ++i) acc[i] = 0.f;
-      for (int j0 = 0; j0 < KB; j0 += 4) {
-        const float sc[4] = {xn.x * wn.x, xn.y * wn.y, xn.z * wn.z, xn.w * wn.w};
-        if (j0 + 4 >= KB) {  // the next tile's (past the last tile: any place inside)
-          const int next = min(tile + step, p.num_tiles - 1);
-          mt_next = next % p.m_tiles;
-          nt_next = next / p.m_tiles;
-          scales_of(mt_next, nt_next);
-        }
-        fetch(xn, wn);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (j0 + u >= KB) break;
+        for (int i = 0; i < FC; ++i) acc[i] = 0.f;
+        auto block = [&](float s, auto&& before) {  // the next accumulator's part of the sums
           ok = timed_wait(&acc_full[b], b_par, wc) && ok;
           __syncwarp();
           tc_fence_after();
           const uint32_t t = taddr + (uint32_t)(b * BN);
+          before(t);
           if constexpr (FC == 128) {
-            fold64(t, sc[u], acc);
-            fold64(t + 64, sc[u], acc + 64);
+            fold64(t, s, acc);
+            fold64(t + 64, s, acc + 64);
           } else if constexpr (FC == 64) {
-            fold64(t, sc[u], acc);
+            fold64(t, s, acc);
           } else {
-            fold32(t, sc[u], acc);
+            fold32(t, s, acc);
           }
           tc_fence_before();
           __syncwarp();
@@ -489,66 +507,105 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
             b = 0;
             b_par ^= 1;
           }
-        }
-        ok = __all_sync(0xffffffffu, ok);  // an expired wait: its sums are not stored
-        if (!ok) break;
-      }
-      if (!ok) break;
-      if constexpr (SPLIT) {  // every load and product of this CTA is complete: the sums go where the stages were
-        float* part = (float*)stages + (32 * q + lane) * T::kPartLd + FC * h;
-#pragma unroll
-        for (int i = 0; i < FC; i += 4) *(float4*)(part + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-        break;
-      }
-      // A thread has a row, and rows lie far apart in memory: OC columns of the warp's 32 rows go through shared memory
-      // (16-byte pieces, swizzled by the row).  64 columns leave by a bulk tensor store, which the next tile's folds need
-      // not wait for; 32 columns by neighbouring lanes that write a row's neighbouring pieces.
-      constexpr int PIECES = OC / 8;  // of a row
-      uint8_t* mine = sm_out + warp * T::kOut;
-#pragma unroll
-      for (int c = 0; c < FC; c += OC) {
-        if (OC == 64 && lane == 0) bulk_wait_read<0>();  // the store before has read its source
-        __syncwarp();
-#pragma unroll
-        for (int v = 0; v < PIECES; ++v) {
-          float4 b0 = make_float4(0.f, 0.f, 0.f, 0.f), b1 = b0;
-          if (n0 + c + 8 * v < p.N && SVDQ_INB(p.status, 4ll * (n0 + c + 8 * v), 32, 4ll * p.N)) {
-            b0 = __ldg((const float4*)(p.bias + n0 + c + 8 * v));
-            b1 = __ldg((const float4*)(p.bias + n0 + c + 8 * v) + 1);
+        };
+        if constexpr (far.value) {
+          for (int j = 0; j < KB && ok; ++j) {
+            const long long ax = (long long)min(m0 + lane, p.M - 1) * p.ld + j_first + j;
+            const long long aw = (long long)min(n0 / kBlk, p.NB - 1) * p.ld + j_first + j;
+            float x = 0.f, w = 0.f;
+            if (SVDQ_INB(p.status, 4 * ax, 4, 4ll * p.M * p.ld) && SVDQ_INB(p.status, 4 * aw, 4, 4ll * p.NB * p.ld)) {
+              x = p.sx[ax];
+              w = __ldg(p.sw + aw);
+            }
+            const bool past = past_f32(x * w);
+            block(past ? fmaxf(x, w) : x * w, [&](uint32_t t) {
+              if (__any_sync(0xffffffffu, past)) scale_columns(t, FC, [&](int) { return past ? fminf(x, w) : 1.f; });
+            });
+            ok = __all_sync(0xffffffffu, ok);
           }
-          const float bb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            __nv_bfloat162 hv = __floats2bfloat162_rn(acc[c + 8 * v + 2 * e] + bb[2 * e],
-                                                      acc[c + 8 * v + 2 * e + 1] + bb[2 * e + 1]);
-            o[e] = *(uint32_t*)&hv;
-          }
-          *(uint4*)(mine + lane * (OC * 2) + ((v ^ lane) & (PIECES - 1)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-        if constexpr (OC == 64) {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && m0 < p.M && n0 + c < p.N) {  // rows and columns past the last are clipped
-            tma_store_2d(&maps.y, mine, n0 + c, m0);
-            bulk_commit();
-          }
+          mt_next = (tile + step) % p.m_tiles;
+          nt_next = (tile + step) / p.m_tiles;
         } else {
-          __syncwarp();
-          const int piece = lane & (PIECES - 1), n = n0 + c + 8 * piece;
-          constexpr int ROWS = 32 / PIECES;  // rows to an instruction
+          for (int j0 = 0; j0 < KB; j0 += 4) {
+            const float sc[4] = {xn.x * wn.x, xn.y * wn.y, xn.z * wn.z, xn.w * wn.w};
+            if (j0 + 4 >= KB) {  // the next tile's (past the last tile: any place inside)
+              const int next = min(tile + step, p.num_tiles - 1);
+              mt_next = next % p.m_tiles;
+              nt_next = next / p.m_tiles;
+              scales_of(mt_next, nt_next);
+            }
+            fetch(xn, wn);
 #pragma unroll
-          for (int i = 0; i < PIECES; ++i) {
-            const int r = ROWS * i + lane / PIECES;
-            const uint4 y = *(const uint4*)(mine + r * (OC * 2) + ((piece ^ r) & (PIECES - 1)) * 16);
-            const long long at = (long long)(m0 + r) * p.N + n;
-            if (m0 + r < p.M && n < p.N && SVDQ_INB(p.status, 2 * at, 16, 2ll * p.M * p.N)) *(uint4*)(p.Y + at) = y;
+            for (int u = 0; u < 4; ++u) {
+              if (j0 + u >= KB) break;
+              block(sc[u], [](uint32_t) {});
+            }
+            ok = __all_sync(0xffffffffu, ok);  // an expired wait: its sums are not stored
+            if (!ok) break;
           }
-          __syncwarp();
         }
+        if (!ok) break;
+        if constexpr (SPLIT) {  // every load and product of this CTA is complete: the sums go where the stages were
+          float* part = (float*)stages + (32 * q + lane) * T::kPartLd + FC * h;
+#pragma unroll
+          for (int i = 0; i < FC; i += 4) *(float4*)(part + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+          break;
+        }
+        // A thread has a row, and rows lie far apart in memory: OC columns of the warp's 32 rows go through shared memory
+        // (16-byte pieces, swizzled by the row).  64 columns leave by a bulk tensor store, which the next tile's folds need
+        // not wait for; 32 columns by neighbouring lanes that write a row's neighbouring pieces.
+        constexpr int PIECES = OC / 8;  // of a row
+        uint8_t* mine = sm_out + warp * T::kOut;
+#pragma unroll
+        for (int c = 0; c < FC; c += OC) {
+          if (OC == 64 && lane == 0) bulk_wait_read<0>();  // the store before has read its source
+          __syncwarp();
+#pragma unroll
+          for (int v = 0; v < PIECES; ++v) {
+            float4 b0 = make_float4(0.f, 0.f, 0.f, 0.f), b1 = b0;
+            if (n0 + c + 8 * v < p.N && SVDQ_INB(p.status, 4ll * (n0 + c + 8 * v), 32, 4ll * p.N)) {
+              b0 = __ldg((const float4*)(p.bias + n0 + c + 8 * v));
+              b1 = __ldg((const float4*)(p.bias + n0 + c + 8 * v) + 1);
+            }
+            const float bb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              __nv_bfloat162 hv = __floats2bfloat162_rn(acc[c + 8 * v + 2 * e] + bb[2 * e],
+                                                        acc[c + 8 * v + 2 * e + 1] + bb[2 * e + 1]);
+              o[e] = *(uint32_t*)&hv;
+            }
+            *(uint4*)(mine + lane * (OC * 2) + ((v ^ lane) & (PIECES - 1)) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          if constexpr (OC == 64) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && m0 < p.M && n0 + c < p.N) {  // rows and columns past the last are clipped
+              tma_store_2d(&maps.y, mine, n0 + c, m0);
+              bulk_commit();
+            }
+          } else {
+            __syncwarp();
+            const int piece = lane & (PIECES - 1), n = n0 + c + 8 * piece;
+            constexpr int ROWS = 32 / PIECES;  // rows to an instruction
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+              const int r = ROWS * i + lane / PIECES;
+              const uint4 y = *(const uint4*)(mine + r * (OC * 2) + ((piece ^ r) & (PIECES - 1)) * 16);
+              const long long at = (long long)(m0 + r) * p.N + n;
+              if (m0 + r < p.M && n < p.N && SVDQ_INB(p.status, 2 * at, 16, 2ll * p.M * p.N)) *(uint4*)(p.Y + at) = y;
+            }
+            __syncwarp();
+          }
+        }
+        mt = mt_next;
+        nt = nt_next;
       }
-      mt = mt_next;
-      nt = nt_next;
+    };
+    if (__ldg(p.far) != 0) {
+      tiles(std::true_type{});
+    } else {
+      tiles(std::false_type{});
     }
     if (!SPLIT && OC == 64 && lane == 0) bulk_wait<0>();
   }
@@ -642,6 +699,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_gemm_fp8_few(const __grid_co
   uint64_t* mma_done = acc_empty + T::kBufs;
   uint32_t* tmem_slot = (uint32_t*)(mma_done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  volatile int* wide_flag = abort_flag + 1;  // a product of scales of this CTA is past binary32
   const int warp = warp_index(), lane = threadIdx.x & 31;
   WaitCtl wc{abort_flag, p.status, p.limit};
   const int rank = p.splits > 1 ? (int)cluster_ctarank() : 0;
@@ -660,6 +718,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_gemm_fp8_few(const __grid_co
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
+    *wide_flag = 0;
     fence_mbar_init();
   }
   __syncthreads();
@@ -730,16 +789,33 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_gemm_fp8_few(const __grid_co
       const long long ax = (long long)t * p.ld + j_first + j, aw = (long long)nt * p.ld + j_first + j;
       float v = 0.f;
       if (t < p.M && SVDQ_INB(p.status, 4 * ax, 4, 4ll * p.M * p.ld) &&
-          SVDQ_INB(p.status, 4 * aw, 4, 4ll * p.NB * p.ld))
-        v = p.sx[ax] * __ldg(p.sw + aw);
+          SVDQ_INB(p.status, 4 * aw, 4, 4ll * p.NB * p.ld)) {
+        const float x = p.sx[ax], w = __ldg(p.sw + aw);
+        v = x * w;
+        if (past_f32(v)) {  // the larger, and the smaller comes to the sums
+          v = fmaxf(x, w);
+          *wide_flag = 1;
+        }
+      }
       table[j * BT + t] = v;
     }
     named_bar_sync(1, 128);
+    const bool wide = *wide_flag != 0;
     const uint32_t taddr = tmem + ((uint32_t)(32 * warp) << 16);
     for (int j = 0; j < blocks; ++j) {
       const int b = j % T::kBufs;
       if (!warp_timed_wait(&acc_full[b], (j / T::kBufs) & 1, wc)) break;
       tc_fence_after();
+      if (wide) {
+        scale_columns(taddr + (uint32_t)(b * BT), BT, [&](int t) {
+          const long long ax = (long long)t * p.ld + j_first + j, aw = (long long)nt * p.ld + j_first + j;
+          if (t >= p.M || !SVDQ_INB(p.status, 4 * ax, 4, 4ll * p.M * p.ld) ||
+              !SVDQ_INB(p.status, 4 * aw, 4, 4ll * p.NB * p.ld))
+            return 1.f;
+          const float x = p.sx[ax], w = __ldg(p.sw + aw);
+          return past_f32(x * w) ? fminf(x, w) : 1.f;
+        });
+      }
       uint32_t r[BT];
       tmem_ld_cols(taddr + (uint32_t)(b * BT), r);
       tc_fence_before();
@@ -949,6 +1025,7 @@ int launch_f8_gemm(const svdq_fp8_layer* L, int64_t M, void* Y, uint8_t* ws, cud
   p.sx = (const float*)(ws + w.scales);
   p.ld = (int)f8_scale_ld(L->K);
   p.sw = L->wscales;
+  p.far = L->far;
   p.bias = L->bias;
   p.Y = (uint16_t*)Y;
   p.status = (int*)(ws + w.status);
@@ -1050,6 +1127,8 @@ svdq_status svdq_fp8_pack(int64_t N, int64_t K, const uint8_t* wcodes, const flo
   uint8_t* blob = (uint8_t*)blob_v;
   std::memset(blob, 0, b.wcodes);
   std::memset(blob + b.wcodes + (size_t)N * K, 0, b.total - b.wcodes - (size_t)N * K);
+  const int far = *std::max_element(wscales, wscales + ns) > kFarScale;
+  std::memcpy(blob + b.far, &far, sizeof(far));
   float* bf = (float*)(blob + b.bias);
   for (int64_t n = 0; n < N; ++n) bf[n] = bias ? host::bf16_to_f32(bias[n]) : 0.f;
   const int64_t kb = (K + kBlk - 1) / kBlk, ld = f8_scale_ld(K);
@@ -1084,6 +1163,7 @@ svdq_status svdq_fp8_layer_create(const void* dev_blob, size_t blob_bytes, int64
   L->bias = (const float*)(base + b.bias);
   L->wscales = (const float*)(base + b.wscales);
   L->wcodes = base + b.wcodes;
+  L->far = (const int*)(base + b.far);
   const uint32_t rows[3] = {256, 128, 64};
   for (int i = 0; i < 3; ++i) {
     if (encode_tmap_2d(&L->map_w[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, L->wcodes, (uint64_t)K, (uint64_t)N, (uint64_t)K,

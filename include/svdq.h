@@ -419,7 +419,8 @@ svdq_status svdq_w8a8_read_status(const svdq_w8a8_layer* layer, int64_t M, const
  *   activation: s_x[m,j] for token m and inputs 128j.., from each input,
  *   s = fl32(max(max|v|, 2^-100) / 448),  q = E4M3(clamp(fl32(v * fl32(1/s)), +-448)), round half to even,
  *   Y = bf16( sum_j s_x[m,j] s_w[n/128,j] sum_{k in block j} qx[m,k] qw[n,k] + b[n] ),
- * products and sums in binary32.  A block whose input holds a NaN or an infinity
+ * products and sums in binary32 (a product of scales past it does not make a small
+ * sum infinite or NaN).  A block whose input holds a NaN or an infinity
  * gives NaN in that token's outputs.  Shapes: N >= 8 and N % 8 == 0, K >= 16 and
  * K % 16 == 0 (the last block of either may be short), N <= 2^24, K <= 2^20. */
 typedef struct svdq_fp8_layer svdq_fp8_layer; /* opaque host-side handle */
@@ -431,9 +432,9 @@ svdq_status svdq_fp8_prepare(const uint16_t* W, int64_t N, int64_t K, uint8_t* w
 
 /* Device layout ("fp8 blob"), regions 1024-byte aligned: bias f32 [N] | wscales
  * f32 [ceil(N/128), S], S = ceil(K/128) rounded up to a multiple of 4 (padding
- * zero) | wcodes u8 [N, K] row-major.  bias bf16 [N] or
- * NULL (zeros).  wscales may be any finite, non-negative values (a checkpoint's
- * own); codes other than NaN (0x7F, 0xFF).  Else INVALID_ARG. */
+ * zero) | wcodes u8 [N, K] row-major | int32: 1 if a scale is above 448, else 0.
+ * bias bf16 [N] or NULL (zeros).  wscales may be any finite, non-negative values
+ * (a checkpoint's own); codes other than NaN (0x7F, 0xFF).  Else INVALID_ARG. */
 svdq_status svdq_fp8_packed_size(int64_t N, int64_t K, size_t* bytes);
 svdq_status svdq_fp8_pack(int64_t N, int64_t K, const uint8_t* wcodes, const float* wscales, const uint16_t* bias,
                           void* blob, size_t blob_bytes);

@@ -74,3 +74,60 @@ def test_norm_of_infinities_and_zero_rows():
     keep[1, 2] = keep[2, 3] = keep[3, 1] = False
     ref, bound = ac.norm_rope(x, None, 0.0, None, None, "interleaved")
     ac.check(y[0][keep], ref[0][keep], bound[0][keep])
+
+
+# every kernel of the product: few tokens (16, 32, 64; alone and in clusters), tiles of 64, 128 and 256 columns (alone and
+# in clusters)
+@pytest.mark.parametrize("M,K,N", [(5, 640, 136), (2, 4096, 512), (24, 400, 264), (30, 2048, 768), (60, 2048, 512),
+                                   (100, 4096, 512), (300, 9728, 264), (129, 640, 4616), (300, 400, 520), (700, 512, 2048),
+                                   (1100, 1168, 2312), (2100, 512, 2568)])
+def test_fp8_scales_whose_product_leaves_binary32(M, K, N):
+    """Tokens of 2^60 and more in one block over a weight scale of 2^70: the product of the scales is infinite, the block's
+    sum is 0 or 2^-18, and so the output is an ordinary number or one of about 2^112."""
+    import torch
+
+    import diffusion_transformer_w4a4_b200 as svdq
+
+    g = ac.generator(M + K)
+    qw, sw = ac.fp8_weight(ac.bf16(g, N, K, scale=0.02))
+    rows = torch.arange(N, device="cuda") % 3 == 0
+    at = 256 if K > 256 else 0  # the block
+    qw[:, at:at + 128] = 0
+    qw[rows, at + 1] = 2.0 ** -9  # the smallest code
+    sw[:, at // 128] = 2.0 ** 70
+    codes = qw.float().to(torch.float8_e4m3fn).view(torch.uint8).cpu().numpy()
+    lin = svdq.Fp8Linear(codes, sw.cpu().numpy(), device="cuda:0")
+    x = ac.bf16(g, M, K)
+    x[:, at:at + 128] = 0
+    plain = lin.forward(x).clone()
+    big = torch.arange(M, device="cuda") % 2 == 0
+    x[big, at] = 448 * 2.0 ** 60         # times a code of 0
+    x[big, at + 1] = 2.0 ** 60 * 2.0 ** -9  # the smallest code, times the smallest or 0
+    qx, sx = ac.fp8_quantize(x)
+    assert not torch.isfinite((sx[big][:, at // 128, None] * sw[:, at // 128])).any()
+    y = lin.forward(x)
+    assert lin.status(M) == 0
+    ref, bound = ac.fp8_linear(qx, sx, qw, sw, None)
+    assert torch.isfinite(bound).all() and ref[0, 0].abs() > 2.0 ** 111
+    ac.check(y, ref, bound)
+    assert torch.equal(y[~big], plain[~big])
+
+
+def test_fp8_infinite_inputs_over_large_scales():
+    """An infinite input gives NaN over any weight scale, 0 and the largest among them."""
+    import torch
+
+    import diffusion_transformer_w4a4_b200 as svdq
+
+    N, K = 264, 512
+    g = ac.generator(3)
+    qw, sw = ac.fp8_weight(ac.bf16(g, N, K, scale=0.02))
+    sw[1] = 3.4e38
+    sw[2] = 0.0
+    lin = svdq.Fp8Linear(qw.float().to(torch.float8_e4m3fn).view(torch.uint8).cpu().numpy(), sw.cpu().numpy(),
+                         device="cuda:0")
+    for M in (3, 70, 300):
+        x = ac.bf16(g, M, K)
+        x[1, 5] = float("inf")
+        y = lin.forward(x)
+        assert torch.isnan(y[1]).all() and not y[0, 256:].any() and torch.isfinite(y[0, :128]).all()
