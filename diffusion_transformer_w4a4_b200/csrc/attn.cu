@@ -801,6 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn(const __grid_constant__ At
       const int rows = total / per_row, mine = (rows - split + p.splits - 1) / p.splits;
       const uint32_t a_part = smem_u32(part), a_m = smem_u32(fm), a_l = smem_u32(fl);
       auto place = [&](int row) { return PAIR && row >= tile_rows ? row - tile_rows + 128 : row; };  // of a row's part
+      if (!good) {  // an expired wait: this CTA stores nothing, and the others' rows become NaN
+        for (int i = threadIdx.x; i < (PAIR ? 256 : 128); i += kThreads) fm[i] = fl[i] = __int_as_float(0x7FC00000);
+      }
       cluster_sync();
       if (good) {
         for (int i = threadIdx.x; i < mine; i += kThreads) {

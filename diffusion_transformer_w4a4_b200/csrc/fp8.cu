@@ -621,8 +621,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) k_gemm_fp8(const __grid_const
     const int m0 = tile0 % p.m_tiles * 128, n0 = tile0 / p.m_tiles * BN;
     const int units = min(128, p.M - m0) * (BN / 4), share = join_share(units, p.splits);
     const int first = rank * share, total = min(share, units - first);  // this CTA's (none, if negative)
+    const bool good = *abort_flag == 0;
+    if (!good) {  // an expired wait: the others' sums become NaN
+      for (int i = threadIdx.x; i < 128 * T::kPartLd; i += kGemmThreads) ((float*)stages)[i] = __int_as_float(0x7FC00000);
+    }
     cluster_sync();
-    if (*abort_flag == 0) {
+    if (good) {
       const uint32_t base = smem_u32(stages);
       for (int u0 = threadIdx.x; u0 < total; u0 += U * kGemmThreads) {
         int row[U], n[U];
@@ -838,7 +842,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_gemm_fp8_few(const __grid_co
     tc_fence_after();
     tmem_dealloc(tmem, T::kCols);
   }
-  const bool good = *abort_flag == 0;  // after an expired wait this CTA stores nothing
+  const bool good = *abort_flag == 0;  // after an expired wait this CTA stores nothing, and the others' sums become NaN
   if (p.splits == 1) {
     const int n = nt * 128 + threadIdx.x;
     if (good && warp < 4 && n < p.N && SVDQ_INB(p.status, 4ll * n, 4, 4ll * p.N)) {
@@ -855,7 +859,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_gemm_fp8_few(const __grid_co
   float* part = (float*)stages;  // [BT][128]: every load and product is complete
   if (warp < 4) {
 #pragma unroll
-    for (int t = 0; t < BT; ++t) part[t * 128 + threadIdx.x] = acc[t];
+    for (int t = 0; t < BT; ++t) part[t * 128 + threadIdx.x] = good ? acc[t] : __int_as_float(0x7FC00000);
   }
   cluster_sync();
   if (good) {

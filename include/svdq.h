@@ -461,7 +461,7 @@ svdq_status svdq_fp8_gemm(const svdq_fp8_layer* layer, int64_t M, void* Y, void*
 svdq_status svdq_fp8_forward(const svdq_fp8_layer* layer, const void* X, int64_t M, void* Y, void* ws,
                              size_t ws_bytes, void* stream);
 /* Synchronous read of the workspace status word (SVDQ_ERR_TIMEOUT after a wait
- * ran past its limit). */
+ * ran past its limit; Y is then incomplete: what lacks a part is NaN or as it was). */
 svdq_status svdq_fp8_read_status(const svdq_fp8_layer* layer, int64_t M, const void* ws, size_t ws_bytes,
                                  int* device_status);
 
@@ -534,9 +534,10 @@ typedef struct svdq_attn_args {
  * dim % 8 == 0, 8 <= dim <= 128; heads % kv_heads == 0, heads <= 4096; token and
  * batch counts up to 2^30 (batch * heads * ceil(q_tokens / 128) <= 2^30).  kv_tokens may
  * be 0 (k and v are then not read).  `status` is a device int32, zeroed once by the
- * caller: an in-kernel wait past its limit records SVDQ_ERR_TIMEOUT there.  No
- * workspace; equal calls give equal bits.  Asynchronous on `stream`, on the current
- * device, whose memory every pointer must be. */
+ * caller: an in-kernel wait past its limit records SVDQ_ERR_TIMEOUT there (O is then
+ * incomplete: a row that lacks a part is NaN or as it was).  No workspace; equal calls
+ * give equal bits.  Asynchronous on `stream`, on the current device, whose memory every
+ * pointer must be. */
 svdq_status svdq_cross_attn(const svdq_attn_args* args, int32_t* status, void* stream);
 
 #ifdef __cplusplus
