@@ -787,9 +787,10 @@ class Fp8Linear:
     current CUDA device), from E4M3 weight codes u8 [N,K] (svdq_fp8_prepare, or a
     checkpoint's own), their scales f32 [ceil(N/128), ceil(K/128)] and an optional
     bf16 bias (bits); `forward(x)` maps bf16 [M, K] to bf16 [M, N], enqueued with the
-    layer's device current.  Workspaces are cached per token count, belong to the
-    stream that used them first and are used by one call at a time (calls on several
-    streams take one layer object each)."""
+    layer's device current.  One workspace serves every token count, and one call at
+    a time (calls on several streams take one layer object each): a call with more
+    tokens than any before makes a larger one, memory of the stream it runs on, and
+    the smaller stay, as a captured graph may use them."""
 
     def __init__(self, wcodes, wscales, bias=None, device=None):
         import torch
@@ -801,36 +802,47 @@ class Fp8Linear:
             self.handle = svdq_fp8_layer_create(self.blob, self.blob.numel(), self.N, self.K)
         self._handle = self.handle.value
         self._blob_stream = torch.cuda.current_stream(self.device).cuda_stream
-        self._ws = {}  # token count: (workspace, handle of the stream whose memory it is, weights, theirs)
+        self._room = None  # (buffer, handle of the stream whose memory it is, weights, theirs)
+        self._smaller = []
 
     def workspace_size(self, M: int) -> int:
         return svdq_fp8_workspace_size(self.handle, M)
 
     def workspace(self, M: int):
-        if M not in self._ws:
+        """The workspace of a call with M tokens: the end of the buffer, so that the status word, a workspace's last 16
+        bytes, has one place whatever M."""
+        size = self.workspace_size(M)
+        have = self._room[0].numel() if self._room else 0
+        if have < size:
             torch = _torch()
-            ws = torch.empty(self.workspace_size(M), dtype=torch.uint8, device=self.device)
-            self._ws[M] = ws, torch.cuda.current_stream(self.device).cuda_stream, self.blob, self._blob_stream
-        return self._ws[M][0]
+            # Half as much again as the one before: all of them come to 4.5 times what the largest call needs at most.
+            buf = torch.empty(16 + max(size - 16, (have // 1024 * 3 + 1) // 2 * 1024), dtype=torch.uint8, device=self.device)
+            buf[-16:].zero_()  # no call yet: status 0
+            if self._room:
+                self._smaller.append(self._room)
+            self._room = buf, torch.cuda.current_stream(self.device).cuda_stream, self.blob, self._blob_stream
+        buf = self._room[0]
+        return buf[buf.numel() - size:]
 
     def forward(self, x, out=None, stream=None):
         if stream is not None:  # what the call allocates, a workspace among it, is memory of the stream that writes it
             with _stream_context(stream, self.device):
                 return self.forward(x, out)
         forward = (_calls_module or _calls()).fp8_forward
-        y = forward(self._handle, self.N, self.K, self.device.index, self._ws, x, out)
-        if y is None:  # the first call with this many tokens
+        y = forward(self._handle, self.N, self.K, self.device.index, self._room, x, out)
+        if y is None:  # the first call with so many tokens
             self.workspace(x.numel() // self.K)
-            y = forward(self._handle, self.N, self.K, self.device.index, self._ws, x, out)
+            y = forward(self._handle, self.N, self.K, self.device.index, self._room, x, out)
         return y
 
     __call__ = forward
 
     def status(self, M: int) -> int:
+        """The status word of the layer's last call (waits for the device)."""
         return svdq_fp8_read_status(self.handle, M, self.workspace(M))
 
     def read_act(self, M: int):
-        """Activation codes u8 [M, K] and scales f32 [M, ceil(K/128)] from the workspace (after quantize_act)."""
+        """Activation codes u8 [M, K] and scales f32 [M, ceil(K/128)] of the layer's last call, which had M tokens."""
         ws = self.workspace(M).cpu().numpy()
         kb = (self.K + 127) // 128
         ld = (kb + 3) // 4 * 4
@@ -865,8 +877,8 @@ def _calls():
             raise RuntimeError("_marshal.so is missing or does not load: build it with "
                                "`python -m diffusion_transformer_w4a4_b200.build`") from e
         address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
-        m.bind(address(L.svdq_qk_norm_rope), address(L.svdq_cross_attn), address(L.svdq_fp8_forward), SvdqError,
-               attn_status, torch.OutOfMemoryError)
+        m.bind(address(L.svdq_qk_norm_rope), address(L.svdq_cross_attn), address(L.svdq_fp8_forward),
+               address(L.svdq_fp8_workspace_size), SvdqError, attn_status, torch.OutOfMemoryError)
         _calls_module = m
     return _calls_module
 

@@ -137,14 +137,17 @@ class FluxBlock:
         self.theta, self._ropes, self.device = theta, [], self.up.device
 
     def _table(self, tokens: int):
-        """Cosines and sines of the first `tokens` rows; a longer table than any before is made once, and waited for."""
+        """Cosines and sines of the first `tokens` rows or more.  A table for more tokens than any before is made once (half
+        as long again as the one before: all of them come to 4.5 times what the longest call needs at most), and waited
+        for."""
         import torch
 
         t = self._ropes[-1] if self._ropes else None
         if t is None or t.shape[0] < tokens:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError(f"no rotation table for {tokens} tokens yet: run the block once before the capture")
-            t = rope_table(tokens, self.attention.dim, self.theta, self.up.device)
+            rows = max(tokens, t.shape[0] * 3 // 2 if t is not None else 0)
+            t = rope_table(rows, self.attention.dim, self.theta, self.up.device)
             torch.cuda.current_stream(self.up.device).synchronize()  # before any other stream uses it
             self._ropes.append(t)  # the shorter ones stay: a captured graph may read them
         return t

@@ -23,6 +23,7 @@ namespace {
 decltype(&svdq_qk_norm_rope) g_norm = nullptr;
 decltype(&svdq_cross_attn) g_attn = nullptr;
 decltype(&svdq_fp8_forward) g_fp8 = nullptr;
+decltype(&svdq_fp8_workspace_size) g_fp8_size = nullptr;
 PyObject* g_error = nullptr;      // SvdqError(status, where)
 PyObject* g_new_status = nullptr;  // attn_status(device index), which calls set_status
 PyObject* g_out_of_memory = nullptr;  // torch.OutOfMemoryError
@@ -113,6 +114,14 @@ void note_use(const at::Tensor& t, void* owner, const c10::cuda::CUDAStream& str
   t.record_stream(stream);
 }
 
+[[noreturn]] void raise_status(int status, const char* where) {
+  PyObject* e = PyObject_CallFunction(g_error, "is", status, where);
+  if (e) {
+    PyErr_SetObject(g_error, e);
+    Py_DECREF(e);
+  }
+  throw PyError();
+}
 // call() with `device` current; a status other than SVDQ_OK raises.
 template <class F>
 void run(const c10::Device& device, const char* where, F&& call) {
@@ -122,13 +131,7 @@ void run(const c10::Device& device, const char* where, F&& call) {
   Py_BEGIN_ALLOW_THREADS;
   st = call();
   Py_END_ALLOW_THREADS;
-  if (st == SVDQ_OK) return;
-  PyObject* e = PyObject_CallFunction(g_error, "is", st, where);
-  if (e) {
-    PyErr_SetObject(g_error, e);
-    Py_DECREF(e);
-  }
-  throw PyError();
+  if (st != SVDQ_OK) raise_status(st, where);
 }
 
 template <class F>
@@ -262,8 +265,9 @@ PyObject* cross_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// fp8_forward(handle, N, K, device index, memory by token count, x, out) -> y on the device's current stream, or None
-// where there is no workspace yet.  The memory: (workspace, handle of its stream, weights, handle of theirs).
+// fp8_forward(handle, N, K, device index, memory, x, out) -> y on the device's current stream, or None where there is no
+// workspace for so many tokens yet.  The memory: (buffer whose end is the workspace, handle of its stream, weights, handle of
+// theirs), or None.
 PyObject* fp8_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 7, [&]() -> PyObject* {
     const auto* layer = (const svdq_fp8_layer*)PyLong_AsVoidPtr(a[0]);
@@ -275,18 +279,16 @@ PyObject* fp8_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse("expected a contiguous bf16 CUDA tensor [..., ", K, "], got ", x.scalar_type(), " ", x.sizes());
     if (x.device() != device) refuse("input on ", x.device(), ", layer on ", device);
     const int64_t M = x.numel() / K;
-    PyObject* key = PyLong_FromLongLong(M);
-    if (!key) throw PyError();
-    PyObject* w = PyDict_GetItemWithError(a[4], key);
-    Py_DECREF(key);
-    if (!w) {
-      if (PyErr_Occurred()) throw PyError();
-      Py_RETURN_NONE;
-    }
-    if (!PyTuple_Check(w) || PyTuple_GET_SIZE(w) != 4) refuse("memory of ", M, " tokens: expected a tuple of four");
-    const at::Tensor &ws = tensor("workspace", PyTuple_GET_ITEM(w, 0)), &blob = tensor("weights", PyTuple_GET_ITEM(w, 2));
-    void *const ws_owner = PyLong_AsVoidPtr(PyTuple_GET_ITEM(w, 1)), *const blob_owner = PyLong_AsVoidPtr(PyTuple_GET_ITEM(w, 3));
+    PyObject* const w = a[4];
+    if (w == Py_None) Py_RETURN_NONE;
+    if (!PyTuple_Check(w) || PyTuple_GET_SIZE(w) != 4) refuse("memory: expected a tuple of four");
+    const at::Tensor &buf = tensor("buffer", PyTuple_GET_ITEM(w, 0)), &blob = tensor("weights", PyTuple_GET_ITEM(w, 2));
+    void *const buf_owner = PyLong_AsVoidPtr(PyTuple_GET_ITEM(w, 1)), *const blob_owner = PyLong_AsVoidPtr(PyTuple_GET_ITEM(w, 3));
     if (PyErr_Occurred()) throw PyError();
+    size_t size = 0;
+    if (const int st = g_fp8_size(layer, M, &size)) raise_status(st, "svdq_fp8_workspace_size");
+    if ((size_t)buf.numel() < size) Py_RETURN_NONE;
+    uint8_t* const ws = (uint8_t*)buf.data_ptr() + ((size_t)buf.numel() - size);
     at::Tensor made;
     const at::Tensor* y = &made;
     if (a[6] == Py_None) {
@@ -297,26 +299,27 @@ PyObject* fp8_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
         refuse("expected a contiguous bf16 output [", M, ", ", N, "] on ", device);
     }
     const c10::cuda::CUDAStream stream = c10::cuda::getCurrentCUDAStream(device.index());
-    note_use(ws, ws_owner, stream);
+    note_use(buf, buf_owner, stream);
     note_use(blob, blob_owner, stream);
     run(device, "svdq_fp8_forward", [&] {
-      return g_fp8(layer, x.data_ptr(), M, y->data_ptr(), ws.data_ptr(), (size_t)ws.numel(), (void*)stream.stream());
+      return g_fp8(layer, x.data_ptr(), M, y->data_ptr(), ws, size, (void*)stream.stream());
     });
     return a[6] == Py_None ? THPVariable_Wrap(made) : Py_NewRef(a[6]);
   });
 }
 
-// bind(addresses of svdq_qk_norm_rope, svdq_cross_attn and svdq_fp8_forward, SvdqError, attn_status,
-//      torch.OutOfMemoryError)
+// bind(addresses of svdq_qk_norm_rope, svdq_cross_attn, svdq_fp8_forward and svdq_fp8_workspace_size, SvdqError,
+//      attn_status, torch.OutOfMemoryError)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 6, [&]() -> PyObject* {
+  return guarded(n, 7, [&]() -> PyObject* {
     g_norm = (decltype(g_norm))PyLong_AsVoidPtr(a[0]);
     g_attn = (decltype(g_attn))PyLong_AsVoidPtr(a[1]);
     g_fp8 = (decltype(g_fp8))PyLong_AsVoidPtr(a[2]);
+    g_fp8_size = (decltype(g_fp8_size))PyLong_AsVoidPtr(a[3]);
     if (PyErr_Occurred()) throw PyError();
-    g_error = Py_NewRef(a[3]);
-    g_new_status = Py_NewRef(a[4]);
-    g_out_of_memory = Py_NewRef(a[5]);
+    g_error = Py_NewRef(a[4]);
+    g_new_status = Py_NewRef(a[5]);
+    g_out_of_memory = Py_NewRef(a[6]);
     Py_RETURN_NONE;
   });
 }
