@@ -874,11 +874,12 @@ def _calls():
         try:
             from . import _marshal as m
         except ImportError as e:
-            raise RuntimeError("_marshal.so is missing or does not load: build it with "
+            raise RuntimeError(f"_marshal.so is missing or does not load ({e}): build it with "
                                "`python -m diffusion_transformer_w4a4_b200.build`") from e
         address = lambda f: ctypes.cast(f, ctypes.c_void_p).value
         m.bind(address(L.svdq_qk_norm_rope), address(L.svdq_cross_attn), address(L.svdq_fp8_forward),
-               address(L.svdq_fp8_workspace_size), SvdqError, attn_status, torch.OutOfMemoryError)
+               address(L.svdq_fp8_workspace_size), SvdqError, attn_status, torch.OutOfMemoryError,
+               str(torch.__version__))
         _calls_module = m
     return _calls_module
 

@@ -13,6 +13,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <cstring>
 #include <exception>
 #include <string>
 
@@ -309,9 +310,19 @@ PyObject* fp8_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // bind(addresses of svdq_qk_norm_rope, svdq_cross_attn, svdq_fp8_forward and svdq_fp8_workspace_size, SvdqError,
-//      attn_status, torch.OutOfMemoryError)
+//      attn_status, torch.OutOfMemoryError, torch.__version__).  Tensors are read by their layout in the torch that this was
+// compiled against: another one is refused.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 7, [&]() -> PyObject* {
+  return guarded(n, 8, [&]() -> PyObject* {
+    const char* torch_version = PyUnicode_AsUTF8(a[7]);
+    if (!torch_version) throw PyError();
+    if (std::strcmp(torch_version, SVDQ_TORCH_VERSION) != 0) {
+      PyErr_Format(PyExc_RuntimeError,
+                   "_marshal.so was built for torch " SVDQ_TORCH_VERSION ", this is %s: build it again with "
+                   "`python -m diffusion_transformer_w4a4_b200.build`",
+                   torch_version);
+      throw PyError();
+    }
     g_norm = (decltype(g_norm))PyLong_AsVoidPtr(a[0]);
     g_attn = (decltype(g_attn))PyLong_AsVoidPtr(a[1]);
     g_fp8 = (decltype(g_fp8))PyLong_AsVoidPtr(a[2]);
@@ -344,4 +355,10 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module_def); }
+PyMODINIT_FUNC PyInit__marshal() {
+  if (Py_Version >> 16 != PY_VERSION_HEX >> 16) {
+    PyErr_SetString(PyExc_ImportError, "built for Python " PY_VERSION);
+    return nullptr;
+  }
+  return PyModule_Create(&module_def);
+}
