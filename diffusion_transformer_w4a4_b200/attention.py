@@ -126,11 +126,14 @@ class CrossAttention:
 
 class FluxBlock:
     """The image stream's linears of a FLUX-style block with their attention, from the layers of a packed checkpoint
-    (`compress.load`): to_qkv -> attention -> to_out -> MLP up -> GELU -> down.  (Residuals, modulation and the block's
-    normalizations belong to the caller.)"""
+    (`compress.load`): to_qkv -> attention -> to_out -> MLP up -> GELU -> down.  q_norm and k_norm are bf16 [dim] weights of
+    the head norms or None.  Tokens are rotated by their number, or by the caller's table (a row for each token of, say,
+    several axes' angles side by side).  (Residuals, modulation and the block's normalizations belong to the caller.)"""
 
-    def __init__(self, layers: dict, heads: int, theta: float = 10000.0, prefix: str = "transformer_blocks.0."):
-        self.attention = SelfAttention(layers[prefix + "attn.to_qkv"], layers[prefix + "attn.to_out.0"], heads)
+    def __init__(self, layers: dict, heads: int, theta: float = 10000.0, prefix: str = "transformer_blocks.0.", q_norm=None,
+                 k_norm=None, eps: float = 1e-6):
+        self.attention = SelfAttention(layers[prefix + "attn.to_qkv"], layers[prefix + "attn.to_out.0"], heads, q_norm,
+                                       k_norm, eps)
         self.up, self.down = layers[prefix + "ff.net.0.proj"], layers[prefix + "ff.net.2"]
         if svdq_mlp_fusable(self.up.handle, self.down.handle) != SVDQ_OK:
             raise ValueError("the MLP pair's shapes or formats cannot be fused (both NVFP4, static scale)")
@@ -153,11 +156,14 @@ class FluxBlock:
         return t
 
     @_on_stream
-    def forward(self, x):
+    def forward(self, x, rope=None, positions=None):
+        """x bf16 [B, S, K] -> [B, S, down.N]; rope and positions as in svdq_qk_norm_rope (rope: by the token's number)."""
         import torch
 
         b, s = _tokens(x, self.attention.to_qkv)
-        h = self.attention.forward(x, rope=self._table(s))
+        if rope is None and positions is not None:
+            raise ValueError("positions need a rope table")
+        h = self.attention.forward(x, rope=self._table(s) if rope is None else rope, positions=positions)
         y = x.new_empty(b * s, self.down.N)
         with torch.cuda.device(self.up.device):
             svdq_mlp_forward(self.up.handle, self.down.handle, h, b * s, y, self.up.workspace(b * s),

@@ -194,6 +194,7 @@ _FMT_CODES = {"int4": 1, "nvfp4": 2}  # svdq_format values of include/svdq.h
 _SVDQ_FIELDS = ("lambda_", "inv_lambda", "L1", "L2", "wcodes", "wscales", "bias")
 _AWQ_FIELDS = ("s", "inv_s", "wcodes", "wscales", "bias")
 _FP8_FIELDS = ("wcodes", "wscales", "bias")
+_NORM_FIELDS = ("q_norm", "k_norm")
 
 
 def _align(n: int) -> int:
@@ -203,8 +204,9 @@ def _align(n: int) -> int:
 def pack(path: str, plans, canon: dict, layers=None, attention: dict | None = None) -> dict:
     """Write the packed checkpoint; `layers` (optional) also stores the bf16
     weights of the layers kept in bf16 so the file describes the whole model, and
-    `attention` (optional: heads, theta) what a block's attention needs besides.
-    Returns the header."""
+    `attention` (optional) what a block's attention needs besides: heads, theta and,
+    where it has them, eps and the bf16 bits [dim] of the head norms' weights,
+    q_norm and k_norm.  Returns the header."""
     specs = {s.name: s for s in (layers or [])}
     entries, blobs = [], []
     off = 0
@@ -237,7 +239,8 @@ def pack(path: str, plans, canon: dict, layers=None, attention: dict | None = No
         entries.append(e)
     header = {"format": "svdq pack", "version": VERSION, "align": ALIGN, "layers": entries}
     if attention is not None:
-        header["attention"] = attention
+        header["attention"] = {f: add(np.asarray(v, np.uint16)) if f in _NORM_FIELDS else v
+                               for f, v in attention.items() if v is not None}
     hbytes = json.dumps(header).encode()
     base = _align(len(MAGIC) + 8 + len(hbytes))
     with open(path, "wb") as f:
@@ -252,7 +255,8 @@ def pack(path: str, plans, canon: dict, layers=None, attention: dict | None = No
 
 def read_packed(path: str):
     """(header, {name: canonical dict}) from a packed checkpoint, on the host.
-    bf16 layers come back as {"W": ..., "bias": ...}."""
+    bf16 layers come back as {"W": ..., "bias": ...}, norm weights as arrays in
+    header["attention"]."""
     raw = np.fromfile(path, dtype=np.uint8)
     if raw[:8].tobytes() != MAGIC:
         raise ValueError(f"{path}: not an svdq pack file")
@@ -261,11 +265,15 @@ def read_packed(path: str):
         raise ValueError(f"{path}: pack version {version}, this reader knows {VERSION}")
     header = json.loads(raw[16:16 + hlen].tobytes().decode())
     base = _align(16 + hlen)
+
+    def array(o, n, dt, shape):
+        return raw[base + o:base + o + n].view(np.dtype(dt)).reshape(shape).copy()
+
+    attention = header.get("attention", {})
+    attention.update({f: array(*attention[f]) for f in _NORM_FIELDS if f in attention})
     out = {}
     for e in header["layers"]:
-        arrays = {}
-        for f, (o, n, dt, shape) in e.get("arrays", {}).items():
-            arrays[f] = raw[base + o:base + o + n].view(np.dtype(dt)).reshape(shape).copy()
+        arrays = {f: array(*rec) for f, rec in e.get("arrays", {}).items()}
         if e["kind"] == SVDQ:
             arrays.update(N=e["N"], K=e["K"], rank=e["rank"], fmt=_FMT_CODES[e["fmt"]], alpha=e["alpha"],
                           g_x=e["g_x"], g_w=e["g_w"])
@@ -299,13 +307,18 @@ def load(path: str, device=None) -> dict:
 
 def load_block(path: str, device=None, prefix: str = "transformer_blocks.0."):
     """attention.FluxBlock of a packed checkpoint that holds its attention's description."""
+    import torch
+
+    from . import _layer_device
     from .attention import FluxBlock
 
     header, _ = read_packed(path)
     if "attention" not in header:
         raise ValueError(f"{path}: packed without its attention (heads)")
     a = header["attention"]
-    return FluxBlock(load(path, device), int(a["heads"]), float(a["theta"]), prefix)
+    norms = {f: torch.from_numpy(a[f].view(np.int16)).view(torch.bfloat16).to(_layer_device(device))
+             for f in _NORM_FIELDS if f in a}
+    return FluxBlock(load(path, device), int(a["heads"]), float(a["theta"]), prefix, eps=float(a.get("eps", 1e-6)), **norms)
 
 
 def compress(layers, inputs: dict, path: str, rank: int = 32, fmt: str = "nvfp4", alpha: float = 0.5,
@@ -328,9 +341,9 @@ def _f32_to_bf16_bits(a):
     return ((u + 0x7FFF + ((u >> 16) & 1)) >> 16).astype(np.uint16)
 
 
-def dense_attention(qkv_bits, heads: int, theta: float = 10000.0, eps: float = 1e-6):
-    """The block's attention on the host, from and to bf16 bits: RMS norm of each head of q and k, rotation of adjacent
-    pairs by the token's position, softmax(q k^T / sqrt(dim)) v; binary64 with one rounding after the rotation (the
+def dense_attention(qkv_bits, heads: int, theta: float = 10000.0, eps: float = 1e-6, q_norm=None, k_norm=None):
+    """The block's attention on the host, from and to bf16 bits: RMS norm of each head of q and k (times bf16 weights
+    [dim], if any), rotation of adjacent pairs by the token's position, softmax(q k^T / sqrt(dim)) v; binary64 with one rounding after the rotation (the
     kernels' order) and one at the end.  [S, 3 * heads * dim] -> [S, heads * dim]."""
     S = qkv_bits.shape[0]
     qkv = _bf16_bits_to_f32(qkv_bits).astype(np.float64).reshape(S, 3, heads, -1)
@@ -338,13 +351,15 @@ def dense_attention(qkv_bits, heads: int, theta: float = 10000.0, eps: float = 1
     angle = np.arange(S)[:, None] * theta ** (-np.arange(dim // 2) * 2.0 / dim)[None, :]
     turn = (np.cos(angle) + 1j * np.sin(angle))[:, None, :]
 
-    def norm_turn(x):
+    def norm_turn(x, weight):
         x = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+        if weight is not None:
+            x = x * _bf16_bits_to_f32(np.asarray(weight, np.uint16))
         z = (x[..., 0::2] + 1j * x[..., 1::2]) * turn
         y = np.stack((z.real, z.imag), -1).reshape(x.shape)
         return _bf16_bits_to_f32(_f32_to_bf16_bits(y.astype(np.float32))).astype(np.float64)
 
-    q, k, v = norm_turn(qkv[:, 0]), norm_turn(qkv[:, 1]), qkv[:, 2]
+    q, k, v = norm_turn(qkv[:, 0], q_norm), norm_turn(qkv[:, 1], k_norm), qkv[:, 2]
     out = np.empty_like(v)
     for h in range(heads):
         s = q[:, h] @ k[:, h].T / np.sqrt(dim)
@@ -353,14 +368,15 @@ def dense_attention(qkv_bits, heads: int, theta: float = 10000.0, eps: float = 1
     return _f32_to_bf16_bits(out.reshape(S, -1).astype(np.float32))
 
 
-def synthetic_flux_block(tokens: int = 512, seed: int = 0, width: int = 3072, heads: int = 0):
+def synthetic_flux_block(tokens: int = 512, seed: int = 0, width: int = 3072, heads: int = 0, q_norm=None, k_norm=None):
     """The linear layers of one synthetic FLUX-style double-stream block (image
     stream) with seeded weights ~ N(0, 0.02^2) and biases ~ N(0, 0.01^2), and
     calibration inputs from a dense bf16 forward of the block's linears on seeded
     tokens ~ N(0, 1) with 0.5 % of the channels scaled x50: the adaLN modulation
     linear (input: a per-sample conditioning vector, batch 2), the fused QKV
     projection, the attention output projection (its input: with `heads`, the
-    attention's output; without, the Q slice standing in for it), the MLP
+    attention's output, its head norms times q_norm and k_norm, bf16 bits [dim], if
+    given; without, the Q slice standing in for it), the MLP
     up-projection and, after a GELU, the MLP down-projection."""
     from scipy.special import erf
 
@@ -388,7 +404,8 @@ def synthetic_flux_block(tokens: int = 512, seed: int = 0, width: int = 3072, he
     mod, qkv, out, up, down = layers
     c = tokens_in(2, D)
     x = tokens_in(tokens, D)
-    a = dense_attention(dense(x, qkv), heads) if heads else np.ascontiguousarray(dense(x, qkv)[:, :D])
+    a = dense_attention(dense(x, qkv), heads, q_norm=q_norm, k_norm=k_norm) if heads else \
+        np.ascontiguousarray(dense(x, qkv)[:, :D])
     h_out = dense(a, out)
     g = _bf16_bits_to_f32(dense(h_out, up)).astype(np.float64)
     h_gelu = _f32_to_bf16_bits((0.5 * g * (1.0 + erf(g / np.sqrt(2.0)))).astype(np.float32))
