@@ -206,6 +206,11 @@ def _stream_context(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _current_handle(device) -> int:
+    """The handle of the device's current stream (torch's Python stream objects take microseconds)."""
+    return (_calls_module or _calls()).current_stream(device.index)
+
+
 def _on(stream, device):
     """The stream that a call works on as the current one: what the call allocates is its memory."""
     return contextlib.nullcontext() if stream is None else _stream_context(stream, device)
@@ -838,7 +843,7 @@ class Fp8Linear:
     __call__ = forward
 
     def status(self, M: int) -> int:
-        """The status word of the layer's last call (waits for the device)."""
+        """The status word of the layer's last call, which has to be done."""
         return svdq_fp8_read_status(self.handle, M, self.workspace(M))
 
     def read_act(self, M: int):

@@ -7,16 +7,31 @@
 
 The projections are any of the package's layer classes (SvdqLinear, Fp8Linear, W8A8Linear, ...); between them run
 svdq_qk_norm_rope (in place on the projection's output) and svdq_cross_attn.  Everything is enqueued, and every
-intermediate allocated, on `stream` (default: the current stream), and nothing waits (but FluxBlock's first call of a
-larger token count, for its rotation table).  Like the layers, whose workspaces they use, objects here serve one call
-at a time.
+intermediate allocated, on `stream` (default: the current stream), and the host waits for nothing (but in FluxBlock's
+first call of a larger token count, for its rotation table).  The layers' workspaces serve one call at a time: a call on
+another stream than the object's last call comes after what that stream has been given so far.  (Not in a capture, and
+not after a raw handle's stream, which may be gone: there the caller sees to the order.)
 """
 from __future__ import annotations
 
 import functools
 
-from . import SVDQ_OK, _layer_device, _stream_context, svdq_cross_attn, svdq_mlp_forward, svdq_mlp_fusable, \
+from . import SVDQ_OK, _layer_device, _stream_context, _current_handle, svdq_cross_attn, svdq_mlp_forward, svdq_mlp_fusable, \
     svdq_qk_norm_rope
+
+
+def _after_last_call(self, handle: int):
+    """The current stream, of this handle, waits for the stream of the object's last call, whose kernels use the same
+    workspaces."""
+    import torch
+
+    if torch.cuda.is_current_stream_capturing():
+        return
+    stream = torch.cuda.current_stream(self.device)
+    if self._last is not None:
+        stream.wait_stream(self._last[1])
+    raw = handle != 0 and stream.stream_id == handle
+    self._last = None if raw else (handle, stream)
 
 
 def _on_stream(f):
@@ -25,10 +40,13 @@ def _on_stream(f):
 
     @functools.wraps(f)
     def g(self, *args, stream=None, **kw):
-        if stream is None:
-            return f(self, *args, **kw)
-        with _stream_context(stream, self.device):
-            return f(self, *args, **kw)
+        if stream is not None:
+            with _stream_context(stream, self.device):
+                return g(self, *args, **kw)
+        handle = _current_handle(self.device)
+        if self._last is None or self._last[0] != handle:
+            _after_last_call(self, handle)
+        return f(self, *args, **kw)
 
     return g
 
@@ -60,6 +78,8 @@ class SelfAttention:
     """Attention among a block's own tokens: `to_qkv` maps a token to heads * dim queries, as many keys and as many
     values, `to_out` takes the heads back.  q_norm and k_norm are bf16 [dim] weights of the head norms or None."""
 
+    _last = None  # (handle, stream) of the last call
+
     def __init__(self, to_qkv, to_out, heads: int, q_norm=None, k_norm=None, eps: float = 1e-6,
                  pairs: str = "interleaved"):
         self.dim = _fits(heads, to_qkv.N, 3, "to_qkv")
@@ -87,6 +107,8 @@ class SelfAttention:
 class CrossAttention:
     """Attention over an encoder's states: `to_q` maps a token to heads * dim queries, `to_kv` a state to
     kv_heads * dim keys and as many values (kv_heads: heads, or a divisor of it whose heads are shared)."""
+
+    _last = None  # (handle, stream) of the last call
 
     def __init__(self, to_q, to_kv, to_out, heads: int, kv_heads: int | None = None, q_norm=None, k_norm=None,
                  eps: float = 1e-6, pairs: str = "interleaved"):
@@ -129,6 +151,8 @@ class FluxBlock:
     (`compress.load`): to_qkv -> attention -> to_out -> MLP up -> GELU -> down.  q_norm and k_norm are bf16 [dim] weights of
     the head norms or None.  Tokens are rotated by their number, or by the caller's table (a row for each token of, say,
     several axes' angles side by side).  (Residuals, modulation and the block's normalizations belong to the caller.)"""
+
+    _last = None  # (handle, stream) of the last call
 
     def __init__(self, layers: dict, heads: int, theta: float = 10000.0, prefix: str = "transformer_blocks.0.", q_norm=None,
                  k_norm=None, eps: float = 1e-6):

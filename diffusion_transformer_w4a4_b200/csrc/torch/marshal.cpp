@@ -345,8 +345,16 @@ PyObject* set_status(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// current_stream(device index) -> handle
+PyObject* current_stream(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 1, [&]() -> PyObject* {
+    return PyLong_FromVoidPtr((void*)c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)integer(a[0])).stream());
+  });
+}
+
 PyMethodDef methods[] = {{"bind", (PyCFunction)(void (*)())bind, METH_FASTCALL, nullptr},
                          {"set_status", (PyCFunction)(void (*)())set_status, METH_FASTCALL, nullptr},
+                         {"current_stream", (PyCFunction)(void (*)())current_stream, METH_FASTCALL, nullptr},
                          {"qk_norm_rope", (PyCFunction)(void (*)())qk_norm_rope, METH_FASTCALL, nullptr},
                          {"cross_attn", (PyCFunction)(void (*)())cross_attn, METH_FASTCALL, nullptr},
                          {"fp8_forward", (PyCFunction)(void (*)())fp8_forward, METH_FASTCALL, nullptr},

@@ -151,3 +151,54 @@ def test_first_call_on_a_side_stream_of_the_other_layers(kind):
     torch.cuda.synchronize()
     assert torch.equal(first, lin.forward(x).cpu())
     assert (lin.status() if kind == "awq" else lin.status(M)) == 0
+
+
+@pytest.mark.parametrize("first", ["side", "current"])
+def test_calls_of_one_object_on_two_streams_are_in_order(first):
+    """An attention sublayer's second call, on another stream, comes after the first, which shares its workspaces."""
+    import torch
+
+    import diffusion_transformer_w4a4_b200 as svdq
+    from diffusion_transformer_w4a4_b200.attention import SelfAttention
+
+    svdq.attn_status()
+    mod = SelfAttention(_fp8(256, 3 * 4 * 64, 11), _fp8(4 * 64, 256, 12), 4)
+    g = ac.generator(13)
+    xs = [ac.bf16(g, 2, 150, 256) for _ in range(2)]
+    want = [mod(x) for x in xs]
+    streams = [torch.cuda.Stream(), torch.cuda.current_stream()]
+    if first == "current":
+        streams.reverse()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(streams[0]):
+        torch.cuda._sleep(CYCLES)
+        one = mod(xs[0])
+    with torch.cuda.stream(streams[1]):
+        two = mod(xs[1])
+    streams[1].synchronize()
+    assert streams[0].query()
+    assert torch.equal(one, want[0]) and torch.equal(two, want[1])
+
+
+def test_call_after_a_raw_handle_that_is_gone():
+    import ctypes
+
+    import torch
+
+    import diffusion_transformer_w4a4_b200 as svdq
+    from diffusion_transformer_w4a4_b200.attention import SelfAttention
+
+    svdq.attn_status()
+    rt = ctypes.CDLL("libcudart.so.12")
+    mod = SelfAttention(_fp8(256, 3 * 4 * 64, 11), _fp8(4 * 64, 256, 12), 4)
+    x = ac.bf16(ac.generator(14), 1, 100, 256)
+    want = mod(x)
+    torch.cuda.synchronize()
+    handle = ctypes.c_void_p()
+    assert rt.cudaStreamCreate(ctypes.byref(handle)) == 0
+    got = mod(x, stream=handle.value)
+    torch.cuda.synchronize()
+    equal = torch.equal(got, want)
+    del got
+    assert rt.cudaStreamDestroy(handle) == 0
+    assert equal and torch.equal(mod(x), want)

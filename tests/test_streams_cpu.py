@@ -13,7 +13,7 @@ SECOND = torch.device("cuda", 1)
 
 class FakeStream:
     def __init__(self, handle, device=None):
-        self.cuda_stream, self.device = handle, device
+        self.cuda_stream, self.device, self.stream_id = handle, device, handle
 
 
 @pytest.fixture
@@ -29,6 +29,9 @@ def entered(monkeypatch):
     monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", FakeStream)
     monkeypatch.setattr(torch.cuda, "stream", current)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: seen[-1])
+    monkeypatch.setattr(attention, "_current_handle", lambda device: seen[-1].cuda_stream)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     return seen
 
 
