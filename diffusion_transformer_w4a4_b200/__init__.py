@@ -149,7 +149,8 @@ _EXPORTS = {
                                         ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "svdq_fp8_read_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
                                             ctypes.POINTER(ctypes.c_int)]),
-    # the argument structures are passed as bytes (a packed svdq_norm_rope_args, svdq_attn_args)
+    # (svdq_qk_norm_rope and svdq_cross_attn below go through _marshal.so, by the functions' addresses; called by these
+    # types they take the structures svdq_norm_rope_args and svdq_attn_args as packed bytes)
     "svdq_qk_norm_rope": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_char_p, ctypes.c_int64, ctypes.c_int64,
                                          ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]),
     "svdq_cross_attn": (ctypes.c_int, [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_void_p]),

@@ -133,10 +133,10 @@ __device__ __forceinline__ float offset_of(float m, float c) {
 }
 
 // One tile of one row (a thread each): the row of scores at tensor-memory address t_s becomes P there, m and l and, where
-// the maximum has risen, the row of O at t_o follow.  masked: keys whose bit in w is 0 do not count.  Arrives on
+// the maximum has risen, the row of O at t_o follow.  masked: keys whose bit in w is 0 do not count.  Arrives on `part`
+// when three quarters of P are written (its product starts while the last quarter is computed).
 // A row that is not valid (past the tile's last, where shared memory holds anything) has no say in when the warp rescales:
 // equal calls round alike.
-// `part` when three quarters of P are written (its product starts while the last quarter is computed).
 // The scores are read twice, for the maximum and for the exponentials: a row of 128 in registers leaves too few of
 // the 168 a thread has for the rest, and what then goes through local memory costs more than the second read.
 __device__ __forceinline__ void softmax_tile(uint32_t t_s, uint32_t t_o, bool masked, const uint32_t (&w)[4], float c,

@@ -526,7 +526,9 @@ typedef struct svdq_attn_args {
 /* O[b,s,h,:] = sum_t p_t V[b,t,h',:] / sum_t p_t, p_t = exp(scale * Q[b,s,h,:].K[b,t,h',:]),
  * over the keys t that count, h' = h / (heads / kv_heads).  Products of bf16 values
  * with binary32 sums, softmax in binary32; p is rounded to bf16 for the product
- * with V; a p below 2^-125 of the row's largest counts as 0.  A row without a key
+ * with V.  A p below 2^-117 of the row's largest may count as 0: a p is taken relative to
+ * a maximum in use, which the row's largest so far exceeds by 2^8 at most, and is 0 there
+ * below 2^-125; sums over earlier and other keys are rescaled likewise.  A row without a key
  * (or whose scores are all -inf) gives 0; keys that do not count have no influence,
  * whatever their K and V hold (NaN included).  A NaN or +inf score makes its row NaN,
  * and so does scale * log2(e) * score past binary32; an infinity or NaN in the V of a key
