@@ -13,10 +13,11 @@
 //                   warp's columns (they lie inside one block of 128 rows of W) and the activation scale one number for a
 //                   thread's row, so a fold is one fused multiply-add an element.
 //     k_gemm_fp8      tiles of 128 tokens by 256, 128 or 64 outputs, persistent; or, with fewer tiles than SMs and many
-//                     inputs, a tile to a cluster whose CTAs split the inputs.  4608 x 3072 x 12288: 166 us (2.1 PFLOP/s);
-//                     bound by the fold, which shares tensor memory with the products: a block takes about 800 clocks
-//                     against 512 of products.  Loading 64 columns at a time is what made it fast (32 at a time, the next
-//                     under way meanwhile: 177 us; accumulators freed by halves: 174).
+//                     inputs, a tile to a cluster whose CTAs split the inputs.  4608 x 3072 x 12288: 160 us
+//                     (2.2 PFLOP/s); bound by the fold, which shares tensor memory with the products: a block takes about
+//                     980 clocks against 512 of products (tensor pipe 52 % busy).  Loading 64 columns at a time is what
+//                     made it fast (when that took 166 us: 32 at a time, the next under way meanwhile, 177; accumulators
+//                     freed by halves 174).
 //     k_gemm_fp8_few  up to 64 tokens: bound by the weight (2 x 3072 x 18432: 13.1 us with the quantizer, 4.3 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>

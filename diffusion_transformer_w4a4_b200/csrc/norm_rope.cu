@@ -3,7 +3,7 @@
 //   y = rot( w * x / sqrt(mean x^2 + eps) ),  rot: (a, c) -> (a cos - c sin, a sin + c cos).
 //
 // Bound by memory: every element is read once and written once, 16 bytes (8 elements) to a lane (9216 tokens of 24 + 24
-// heads of 128: 43.7 us, 5.2 TB/s; half-split pairs, whose elements come in two pieces of 8 bytes, 46.4).  A head's row of
+// heads of 128: 44.4 us, 5.1 TB/s; half-split pairs, whose elements come in two pieces of 8 bytes, 47.2).  A head's row of
 // dim elements lies in LG lanes (the power of two >= dim / 8), so the mean is a sum over shuffles and no shared memory
 // is needed.  A CTA takes one token at a time: its lanes keep the token's cosines and sines and the weight in registers
 // and walk the token's heads with them.
