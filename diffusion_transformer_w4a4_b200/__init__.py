@@ -201,7 +201,8 @@ def _stream_context(stream, device):
     """`stream` (a torch stream, or a raw handle of one of `device`) as the current stream of `device`."""
     torch = _torch()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=device)
+        handle = int(getattr(stream, "cuda_stream", stream))  # 0: the default stream (ExternalStream(0) is a new one)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     if stream.device != device:
         raise ValueError(f"a stream of {stream.device} for work on {device}")
     return torch.cuda.stream(stream)

@@ -25,8 +25,9 @@ def _after_last_call(self, handle: int):
     workspaces."""
     import torch
 
-    if torch.cuda.is_current_stream_capturing():
-        return
+    with torch.cuda.device(self.device):
+        if torch.cuda.is_current_stream_capturing():
+            return
     stream = torch.cuda.current_stream(self.device)
     if self._last is not None:
         stream.wait_stream(self._last[1])

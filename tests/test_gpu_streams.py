@@ -202,3 +202,38 @@ def test_call_after_a_raw_handle_that_is_gone():
     del got
     assert rt.cudaStreamDestroy(handle) == 0
     assert equal and torch.equal(mod(x), want)
+
+
+@pytest.mark.parametrize("kind", ["nvfp4", "w8a8", "awq", "fp8", "attention", "norm", "attn"])
+def test_handle_0_is_the_default_stream(kind):
+    """A raw handle of the default stream, which is 0: the work comes after what that stream has yet to do."""
+    import torch
+
+    import diffusion_transformer_w4a4_b200 as svdq
+    from diffusion_transformer_w4a4_b200.attention import SelfAttention
+
+    svdq.attn_status()
+    assert torch.cuda.current_stream().cuda_stream == 0
+    g = ac.generator(21)
+    shape = (300, 512)
+    if kind in ("norm", "attn"):
+        shape = (2, 100, 4, 64)
+        call = (lambda x, **kw: svdq.svdq_qk_norm_rope(x, **kw)) if kind == "norm" else \
+            (lambda x, **kw: svdq.svdq_cross_attn(x, x, x, **kw))
+    elif kind == "attention":
+        shape = (2, 150, 256)
+        call = SelfAttention(_fp8(256, 3 * 4 * 64, 11), _fp8(4 * 64, 256, 12), 4)
+    else:
+        call = (_fp8(512, 384, 22) if kind == "fp8" else _older_layer(kind, 384, 512)).forward
+    src = ac.bf16(g, *shape)
+    want = call(src)
+    torch.cuda.synchronize()
+    if kind in ("nvfp4", "w8a8", "awq"):
+        call = _older_layer(kind, 384, 512).forward  # without a workspace
+        torch.cuda.synchronize()
+    x = torch.zeros_like(src)
+    torch.cuda._sleep(CYCLES)
+    x.copy_(src)
+    got = call(x, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)

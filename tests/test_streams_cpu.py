@@ -29,6 +29,7 @@ def entered(monkeypatch):
     monkeypatch.setattr(torch.cuda, "Stream", FakeStream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", FakeStream)
     monkeypatch.setattr(torch.cuda, "stream", current)
+    monkeypatch.setattr(torch.cuda, "device", lambda device: contextlib.nullcontext())
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: seen[-1])
     monkeypatch.setattr(attention, "_current_handle", lambda device: seen[-1].cuda_stream)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
@@ -39,6 +40,14 @@ def test_raw_handle_is_a_stream_of_the_works_device(entered):
     with svdq._stream_context(0x1234, SECOND):
         pass
     assert [(s.cuda_stream, s.device) for s in entered] == [(0x1234, SECOND)]
+
+
+def test_handle_0_is_the_default_stream(entered, monkeypatch):
+    default = FakeStream(0, SECOND)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device: default if device == SECOND else None)
+    with svdq._stream_context(0, SECOND):
+        pass
+    assert entered == [default]
 
 
 def test_attention_classes_take_the_raw_handle_to_their_device(entered):
