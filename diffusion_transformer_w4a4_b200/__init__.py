@@ -214,7 +214,8 @@ def _current_handle(device) -> int:
 
 
 def _on(stream, device):
-    """The stream that a call works on as the current one: what the call allocates is its memory."""
+    """The stream that a call works on as the current one, for a call that allocates: what it makes is that stream's memory.
+    (Making a stream current costs the host 8 us; None leaves the current one.)"""
     return contextlib.nullcontext() if stream is None else _stream_context(stream, device)
 
 
@@ -458,7 +459,7 @@ class SvdqLinear:
 
         _check_input(x, self.K, self.device)
         M = x.numel() // self.K
-        with torch.cuda.device(self.device), _on(stream, self.device):
+        with torch.cuda.device(self.device), _on(stream if out is None or M not in self._ws else None, self.device):
             y = out if out is not None else torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
             svdq_forward(self.handle, x, M, y, self.workspace(M), stream)
         return y
@@ -570,7 +571,7 @@ class AwqLinear:
 
         _check_input(x, self.K, self.device)
         M = x.numel() // self.K
-        with torch.cuda.device(self.device), _on(stream, self.device):
+        with torch.cuda.device(self.device), _on(stream if out is None else None, self.device):
             y = out if out is not None else torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
             svdq_awq_forward(self.handle, x, M, y, stream)
         return y
@@ -682,13 +683,13 @@ class W8A8Linear:
     def quantize_act(self, x, M: int, stream=None):
         import torch
 
-        with torch.cuda.device(self.device), _on(stream, self.device):
+        with torch.cuda.device(self.device), _on(stream if M not in self._ws else None, self.device):
             svdq_w8a8_quantize_act(self.handle, x, M, self.workspace(M), stream)
 
     def gemm(self, M: int, y, stream=None):
         import torch
 
-        with torch.cuda.device(self.device), _on(stream, self.device):
+        with torch.cuda.device(self.device), _on(stream if M not in self._ws else None, self.device):
             svdq_w8a8_gemm(self.handle, M, y, self.workspace(M), stream)
 
     def forward(self, x, out=None, stream=None):
@@ -696,7 +697,7 @@ class W8A8Linear:
 
         _check_input(x, self.K, self.device)
         M = x.numel() // self.K
-        with torch.cuda.device(self.device), _on(stream, self.device):
+        with torch.cuda.device(self.device), _on(stream if out is None or M not in self._ws else None, self.device):
             y = out if out is not None else torch.empty(M, self.N, dtype=torch.bfloat16, device=x.device)
             svdq_w8a8_forward(self.handle, x, M, y, self.workspace(M), stream)
         return y
@@ -832,14 +833,19 @@ class Fp8Linear:
         return buf[buf.numel() - size:]
 
     def forward(self, x, out=None, stream=None):
-        if stream is not None:  # what the call allocates, a workspace among it, is memory of the stream that writes it
-            with _stream_context(stream, self.device):
-                return self.forward(x, out)
         forward = (_calls_module or _calls()).fp8_forward
-        y = forward(self._handle, self.N, self.K, self.device.index, self._room, x, out)
+        if stream is not None:
+            if out is not None and isinstance(stream, _torch().cuda.Stream) and stream.device == self.device:
+                y = forward(self._handle, self.N, self.K, self.device.index, self._room, x, out, stream.cuda_stream,
+                            stream.stream_id)
+                if y is not None:
+                    return y
+            with _stream_context(stream, self.device):  # what the call allocates is memory of the stream that writes it
+                return self.forward(x, out)
+        y = forward(self._handle, self.N, self.K, self.device.index, self._room, x, out, None, None)
         if y is None:  # the first call with so many tokens
             self.workspace(x.numel() // self.K)
-            y = forward(self._handle, self.N, self.K, self.device.index, self._room, x, out)
+            y = forward(self._handle, self.N, self.K, self.device.index, self._room, x, out, None, None)
         return y
 
     __call__ = forward

@@ -266,11 +266,11 @@ PyObject* cross_attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// fp8_forward(handle, N, K, device index, memory, x, out) -> y on the device's current stream, or None where there is no
-// workspace for so many tokens yet.  The memory: (buffer whose end is the workspace, handle of its stream, weights, handle of
-// theirs), or None.
+// fp8_forward(handle, N, K, device index, memory, x, out, stream, id) -> y, or None where there is no workspace for so many
+// tokens yet.  The memory: (buffer whose end is the workspace, handle of its stream, weights, handle of theirs), or None.
+// With an output the stream may be a handle other than the current stream's, and torch's id of it.
 PyObject* fp8_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 7, [&]() -> PyObject* {
+  return guarded(n, 9, [&]() -> PyObject* {
     const auto* layer = (const svdq_fp8_layer*)PyLong_AsVoidPtr(a[0]);
     const int64_t N = integer(a[1]), K = integer(a[2]);
     const c10::Device device(c10::DeviceType::CUDA, (c10::DeviceIndex)integer(a[3]));
@@ -299,7 +299,11 @@ PyObject* fp8_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (y->scalar_type() != at::kBFloat16 || y->device() != device || !y->is_contiguous() || y->numel() != M * N)
         refuse("expected a contiguous bf16 output [", M, ", ", N, "] on ", device);
     }
-    const c10::cuda::CUDAStream stream = c10::cuda::getCurrentCUDAStream(device.index());
+    const c10::cuda::CUDAStream stream =
+        a[7] == Py_None ? c10::cuda::getCurrentCUDAStream(device.index())
+                        : c10::cuda::CUDAStream::unpack3(integer(a[8]), device.index(), c10::DeviceType::CUDA);
+    if (a[7] != Py_None && (a[6] == Py_None || (void*)stream.stream() != PyLong_AsVoidPtr(a[7])))
+      refuse("not a stream of ", device, " that is known by its id");
     note_use(buf, buf_owner, stream);
     note_use(blob, blob_owner, stream);
     run(device, "svdq_fp8_forward", [&] {

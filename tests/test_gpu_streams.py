@@ -68,7 +68,8 @@ def test_first_call_on_a_side_stream_keeps_its_workspace(raw):
     assert lin.status(M) == 0 and torch.equal(y, lin.forward(x))
 
 
-def test_dropped_layer_waits_for_the_other_stream():
+@pytest.mark.parametrize("explicit", [False, True])
+def test_dropped_layer_waits_for_the_other_stream(explicit):
     """A layer and its workspace, memory of the current stream, used on another one and dropped while that still works:
     neither is handed out."""
     import torch
@@ -82,7 +83,10 @@ def test_dropped_layer_waits_for_the_other_stream():
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
         torch.cuda._sleep(CYCLES)
-        lin.forward(x, out=out)
+        if not explicit:
+            lin.forward(x, out=out)
+    if explicit:
+        lin.forward(x, out=out, stream=side)
     del lin
     again = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in used]
     for t in again:
